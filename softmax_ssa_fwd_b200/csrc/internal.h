@@ -1,4 +1,4 @@
-// internal.h -- host helpers shared by the two kernels of libssa (not part of
+// internal.h -- host helpers shared by the kernels of libssa (not part of
 // the C ABI).
 #pragma once
 #include <cuda.h>
@@ -8,6 +8,9 @@ namespace ssa {
 // [B, L, H, d] bf16 -> 4-D TMA tensor map (d, H, L, B) with a (64, 1, rows, 1)
 // box and 128-byte swizzle; coordinates past the tensor read zeros.
 bool tma_map_bf16(CUtensorMap* map, const void* base, int B, int L, int H, int d, int rows);
+// The same with a (64, heads, rows, 1) box: `heads` neighbouring heads of each
+// of `rows` tokens land as rows * heads consecutive tile rows, token-major.
+bool tma_map_bf16_box(CUtensorMap* map, const void* base, int B, int L, int H, int d, int heads, int rows);
 
 // The per-device status word that a timed-out bounded device wait raises
 // (ssa_device_status reads and clears it); nullptr on failure.

@@ -1187,14 +1187,14 @@ static EncodeTiledFn encode_fn() {
   return g_encode;
 }
 
-// [B, L, H, d] bf16 -> 4-D map (d, H, L, B), box (64, 1, rows, 1), 128B swizzle,
+// [B, L, H, d] bf16 -> 4-D map (d, H, L, B), box (64, heads, rows, 1), 128B swizzle,
 // zero fill outside the tensor (ragged tails read zeros).
-static bool make_map(CUtensorMap* map, const void* base, int B, int L, int H, int d, int rows) {
+static bool make_map(CUtensorMap* map, const void* base, int B, int L, int H, int d, int rows, int heads = 1) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
   cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2, (cuuint64_t)L * H * d * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1216,6 +1216,11 @@ static int* status_word(int dev) {
 bool tma_map_bf16(CUtensorMap* map, const void* base, int B, int L, int H, int d, int rows) {
   std::lock_guard<std::mutex> g(g_mu);
   return make_map(map, base, B, L, H, d, rows);
+}
+
+bool tma_map_bf16_box(CUtensorMap* map, const void* base, int B, int L, int H, int d, int heads, int rows) {
+  std::lock_guard<std::mutex> g(g_mu);
+  return make_map(map, base, B, L, H, d, rows, heads);
 }
 
 int* device_status_word(int dev) {
