@@ -2,8 +2,9 @@
 
 The compute path is the C-ABI library ``libssa.so`` (``include/ssa.h``), built
 from ``csrc/`` for sm_100a.  ``ssa`` is its thin Python binding (argument
-marshalling only); ``inputs`` holds the seeded synthetic workloads.
+marshalling only), ``cache`` that of the key/value cache operators
+(``include/ssa_cache.h``); ``inputs`` holds the seeded synthetic workloads.
 Importing the binding fails loudly when the library is missing: there is no
 fallback.
 """
-__all__ = ["ssa", "inputs", "build"]
+__all__ = ["ssa", "cache", "inputs", "build"]

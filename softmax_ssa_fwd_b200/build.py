@@ -5,9 +5,10 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = [os.path.join(HERE, "csrc", "ssa_fwd.cu"), os.path.join(HERE, "csrc", "ssa_decode.cu")]
-DEPS = SRC + [os.path.join(HERE, "csrc", "ptx.cuh"), os.path.join(HERE, "csrc", "internal.h"),
-              os.path.join(ROOT, "include", "ssa.h")]
+SRC = [os.path.join(HERE, "csrc", f) for f in ("ssa_fwd.cu", "ssa_decode.cu", "ssa_cache.cu", "ssa_tree.cu",
+                                               "ssa_mass.cu")]
+DEPS = SRC + [os.path.join(HERE, "csrc", f) for f in ("ptx.cuh", "sched.cuh", "internal.h")] + \
+       [os.path.join(ROOT, "include", f) for f in ("ssa.h", "ssa_cache.h")]
 LIB = os.path.join(HERE, "libssa.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -1,0 +1,282 @@
+"""ctypes binding of the key/value cache operators of libssa (include/ssa_cache.h).
+
+``append``       normalise and rotate queries and keys, write keys and values into a cache
+``decode_tree``  attention of drafted tokens (a tree, a chain, one token) over caches of different lengths
+``attn_mass``    attention weight that each cached key received
+``evict``        compaction of a cache to its heaviest keys
+
+Marshalling and checks of what a C pointer cannot carry (dtype, device, layout);
+every step runs in the CUDA kernels behind the C ABI and there is no fallback.
+Functions that begin with ``ssa_`` are the C entry points and return their
+status code; the others raise ``SSAError``.  Calls run on the device of the
+tensors and on ``stream``, by default torch's current stream of that device;
+outputs that are not passed in are allocated there.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import NamedTuple
+
+import torch
+
+from .ssa import SSA_ERR_INVALID_ARG, SSA_OK, SSAError, lib
+
+EXPORTED = ["ssa_cache_append", "ssa_decode_tree", "ssa_decode_tree_workspace_bytes", "ssa_attn_mass",
+            "ssa_cache_evict"]
+
+
+def _bind():
+    P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.ssa_cache_append.restype = I
+    lib.ssa_cache_append.argtypes = [P, P, P, P, P, P, F, P, P, P, I, I, I, F, P, P, P, P, P] + [I] * 6 + [P]
+    lib.ssa_decode_tree.restype = I
+    lib.ssa_decode_tree.argtypes = [P] * 7 + [I] * 6 + [F, P, Z, P]
+    lib.ssa_decode_tree_workspace_bytes.restype = Z
+    lib.ssa_decode_tree_workspace_bytes.argtypes = [I] * 6
+    lib.ssa_attn_mass.restype = I
+    lib.ssa_attn_mass.argtypes = [P] * 6 + [I] * 8 + [F, F, P]
+    lib.ssa_cache_evict.restype = I
+    lib.ssa_cache_evict.argtypes = [P] * 9 + [I] * 8 + [P]
+
+
+_bind()
+
+ssa_cache_append = lib.ssa_cache_append
+ssa_decode_tree = lib.ssa_decode_tree
+ssa_decode_tree_workspace_bytes = lib.ssa_decode_tree_workspace_bytes
+ssa_attn_mass = lib.ssa_attn_mass
+ssa_cache_evict = lib.ssa_cache_evict
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise SSAError(SSA_ERR_INVALID_ARG, what)
+
+
+def _tensor(t, name, dtype, shape, device, contiguous=True):
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == device
+          and (not contiguous or t.is_contiguous()),
+          f"{name}: want {'contiguous ' if contiguous else ''}{dtype} {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _optional(t, name, dtype, shape, device):
+    return None if t is None else _tensor(t, name, dtype, shape, device)
+
+
+def _heads(x, name):
+    _need(isinstance(x, torch.Tensor) and x.dim() == 4 and x.dtype == torch.bfloat16 and x.is_cuda,
+          f"{name}: want a 4-dimensional bf16 CUDA tensor")
+    return x.shape
+
+
+class _On:
+    """The device of a call made current, and its stream (torch's allocations inside follow it)."""
+
+    def __init__(self, device, stream):
+        self.stack = contextlib.ExitStack()
+        if torch.cuda.current_device() != device.index:
+            self.stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            _need(stream.device == device, "stream: belongs to another device than the tensors")
+            self.stack.enter_context(torch.cuda.stream(stream))
+        self.device = device
+
+    def __enter__(self):
+        self.stack.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *e):
+        return self.stack.__exit__(*e)
+
+
+def _done(status, what):
+    if status != SSA_OK:
+        raise SSAError(status, what)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original: int = 8192, low: float = 1.0, high: float = 4.0):
+    """(inv_freq, factor) for ``append``: a CPU float64 tensor of rot / 2 radians per position, and what
+    cosine and sine are multiplied by.
+
+    ``scaling``: "none" base^(-2p / rot); "linear" all divided by ``factor``; "base" the base raised by
+    factor^(rot / (rot - 2)), which divides the slowest by ``factor`` and leaves the fastest; "bands" by how often a
+    pair turns within ``original`` positions: at most ``low`` turns divided by ``factor``, at least ``high`` left, between
+    them a straight line between the two in turns; "ramp" the same with the line in the pair's number, and a factor of
+    1 + 0.1 ln(factor) on cosine and sine.
+    """
+    _need(rot > 0 and rot % 2 == 0 and base > 0 and factor > 0, "rope_frequencies: rot even, base and factor positive")
+    n = rot // 2
+    p = torch.arange(n, dtype=torch.float64)
+    if scaling == "base":
+        _need(rot > 2, "rope_frequencies: scaling 'base' needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-p / n)
+    if scaling in ("none", "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    _need(scaling in ("bands", "ramp") and 0 < low < high and original > 0,
+          "rope_frequencies: scaling is none, linear, base, bands or ramp; 0 < low < high")
+    if scaling == "bands":
+        turns = original * f / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        return f * (keep + (1 - keep) / factor), 1.0
+    # the (whole) pair numbers that turn `high` and `low` times
+    at = lambda t: n * math.log(original / (2 * math.pi * t)) / math.log(base)  # noqa: E731
+    first, last = max(0, math.floor(at(high))), min(rot - 1, math.ceil(at(low)))
+    keep = 1 - ((p - first) / max(last - first, 1e-3)).clamp(0, 1)
+    return f * (keep + (1 - keep) / factor), (1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0)
+
+
+def append(q, k, v, k_cache, v_cache, positions=None, *, inv_freq=None, axis=None, interleaved=False, factor=1.0,
+           q_weight=None, k_weight=None, eps=1e-6, start=None, count=None, out=None, stream=None):
+    """Norm and rotation of q [B, L, Hq, d] and k [B, L, Hkv, d], and the write of k and v into rows
+    start[b].. of k_cache, v_cache [B, cap, Hkv, d].  Returns the rotated queries [B, L, Hq, d].
+
+    q, k, v may be strided (slices of one projection).  positions [B, L] or [B, L, axes] int32;
+    inv_freq: CPU float64 [rot / 2] (None: no rotation); axis: CPU int32 [rot / 2]; weights fp32 [d];
+    start, count int32 [B].  ``out`` (may be q): rows of tokens at and past count[b] keep what they hold;
+    without ``out`` they are undefined.
+    """
+    B, L, Hq, d = _heads(q, "q")
+    dev = q.device
+    Hkv = _heads(k, "k")[2]
+    _tensor(k, "k", torch.bfloat16, (B, L, Hkv, d), dev, contiguous=False)
+    _tensor(v, "v", torch.bfloat16, (B, L, Hkv, d), dev, contiguous=False)
+    _need(all(x.stride(3) == 1 for x in (q, k, v)), "q, k, v: the columns of a head have to be contiguous")
+    cap = _heads(k_cache, "k_cache")[1]
+    kc = _tensor(k_cache, "k_cache", torch.bfloat16, (B, cap, Hkv, d), dev)
+    vc = _tensor(v_cache, "v_cache", torch.bfloat16, (B, cap, Hkv, d), dev)
+    rot, axes, freq, ax, pos = 0, 1, None, None, None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        freq = _tensor(inv_freq, "inv_freq", torch.float64, (rot // 2,), torch.device("cpu"))
+        _need(isinstance(positions, torch.Tensor) and positions.dim() in (2, 3), "positions: want [B, L] or [B, L, axes]")
+        axes = positions.shape[2] if positions.dim() == 3 else 1
+        pos = _tensor(positions, "positions", torch.int32, (B, L, axes) if positions.dim() == 3 else (B, L), dev)
+        ax = _optional(axis, "axis", torch.int32, (rot // 2,), torch.device("cpu"))
+    wq = _optional(q_weight, "q_weight", torch.float32, (d,), dev)
+    wk = _optional(k_weight, "k_weight", torch.float32, (d,), dev)
+    s0 = _optional(start, "start", torch.int32, (B,), dev)
+    cnt = _optional(count, "count", torch.int32, (B,), dev)
+    strides = (ctypes.c_int64 * 9)(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(B, L, Hq, d, dtype=torch.bfloat16, device=dev)
+        qo = _tensor(out, "out", torch.bfloat16, (B, L, Hq, d), dev)
+        _done(ssa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, wq, wk, eps, pos, freq, ax, axes, rot,
+                               int(interleaved), factor, s0, cnt, qo, kc, vc, B, L, Hq, Hkv, d, cap, st),
+              "ssa_cache_append")
+    return out
+
+
+def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of T drafted tokens per sequence (q [B, T, Hq, d]) over its cache k, v [B, cap, Hkv, d]:
+    the keys before lens[b], and draft key t (row lens[b] + t) where bit t of tree_mask[b, i] is set.
+
+    lens int32 [B]; tree_mask int32 or uint32 [B, T, ceil(T / 32)].  Returns (out [B, T, Hq, d] bf16,
+    lse [B, Hq, T] fp32).  ``workspace``: uint8, ``ssa_decode_tree_workspace_bytes`` bytes.
+    """
+    B, T, Hq, d = _heads(q, "q")
+    dev = q.device
+    _, cap, Hkv, _ = _heads(k, "k")
+    qp = _tensor(q, "q", torch.bfloat16, q.shape, dev)
+    kp = _tensor(k, "k", torch.bfloat16, (B, cap, Hkv, d), dev)
+    vp = _tensor(v, "v", torch.bfloat16, (B, cap, Hkv, d), dev)
+    lp = _tensor(lens, "lens", torch.int32, (B,), dev)
+    words = (B, T, (T + 31) // 32)
+    mp = _tensor(tree_mask, "tree_mask",
+                 torch.uint32 if getattr(tree_mask, "dtype", None) == torch.uint32 else torch.int32, words, dev)
+    if scale is None:
+        scale = d ** -0.5
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(B, T, Hq, d, dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(16, ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d)), dtype=torch.uint8,
+                                    device=dev)
+        _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: want a contiguous tensor on {dev}")
+        op = _tensor(out, "out", torch.bfloat16, (B, T, Hq, d), dev)
+        sp = _tensor(lse, "lse", torch.float32, (B, Hq, T), dev)
+        _done(ssa_decode_tree(qp, kp, vp, op, sp, lp, mp, B, T, Hq, Hkv, cap, d, scale, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), st), "ssa_decode_tree")
+    return out, lse
+
+
+def attn_mass(q, k, lse, *, lens=None, causal=True, scale=None, window=0, mass=None, decay=1.0, out=None, stream=None):
+    """Attention weight that each key of k [B, cap, Hkv, d] received from the rows q [B, Lq, Hq, d] (the last
+    ``window`` of them; 0: all), given their lse [B, Hq, Lq] from the attention: decay * mass + the sum over rows and
+    the query heads of a key head.  Returns mass [B, Hkv, cap] fp32 (``out``; may be ``mass`` itself), 0 past lens[b].
+    """
+    B, Lq, Hq, d = _heads(q, "q")
+    dev = q.device
+    _, cap, Hkv, _ = _heads(k, "k")
+    qp = _tensor(q, "q", torch.bfloat16, q.shape, dev)
+    kp = _tensor(k, "k", torch.bfloat16, (B, cap, Hkv, d), dev)
+    sp = _tensor(lse, "lse", torch.float32, (B, Hq, Lq), dev)
+    lp = _optional(lens, "lens", torch.int32, (B,), dev)
+    mp = _optional(mass, "mass", torch.float32, (B, Hkv, cap), dev)
+    if scale is None:
+        scale = d ** -0.5
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(B, Hkv, cap, dtype=torch.float32, device=dev)
+        op = _tensor(out, "out", torch.float32, (B, Hkv, cap), dev)
+        _done(ssa_attn_mass(qp, kp, sp, lp, mp, op, B, Lq, window, Hq, Hkv, cap, d, int(causal), scale, decay, st),
+              "ssa_attn_mass")
+    return out
+
+
+class Evicted(NamedTuple):
+    k: torch.Tensor        # [B, cap_out, Hkv, d]
+    v: torch.Tensor
+    mass: torch.Tensor     # [B, Hkv, cap_out]
+    index: torch.Tensor    # [B, Hkv, keep] int32, -1 past the kept
+    lens: torch.Tensor     # [B] int32
+
+
+def evict(k, v, mass, lens, *, keep, sink=0, recent=0, k_out=None, v_out=None, mass_out=None, index=None, new_lens=None,
+          stream=None):
+    """Compact caches k, v [B, cap, Hkv, d] to at most ``keep`` keys a key head: the first ``sink``, the last
+    ``recent`` and the heaviest by mass [B, Hkv, cap] of the rest, in ascending order.  k_out, v_out
+    [B, cap_out, Hkv, d] with cap_out >= keep (default keep); their rows past the kept ones keep what they hold.
+    Returns ``Evicted``.
+    """
+    B, cap, Hkv, d = _heads(k, "k")
+    dev = k.device
+    kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
+    vp = _tensor(v, "v", torch.bfloat16, k.shape, dev)
+    mp = _tensor(mass, "mass", torch.float32, (B, Hkv, cap), dev)
+    lp = _tensor(lens, "lens", torch.int32, (B,), dev)
+    _need(keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep, "keep, sink, recent: want sink + recent <= keep")
+    with _On(dev, stream) as st:
+        cap_out = keep
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None:
+                cap_out = _heads(t, name)[1]
+        if k_out is None:
+            k_out = torch.empty(B, cap_out, Hkv, d, dtype=torch.bfloat16, device=dev)
+        if v_out is None:
+            v_out = torch.empty(B, cap_out, Hkv, d, dtype=torch.bfloat16, device=dev)
+        if mass_out is None:
+            mass_out = torch.empty(B, Hkv, cap_out, dtype=torch.float32, device=dev)
+        if index is None:
+            index = torch.empty(B, Hkv, keep, dtype=torch.int32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        ko = _tensor(k_out, "k_out", torch.bfloat16, (B, cap_out, Hkv, d), dev)
+        vo = _tensor(v_out, "v_out", torch.bfloat16, (B, cap_out, Hkv, d), dev)
+        mo = _tensor(mass_out, "mass_out", torch.float32, (B, Hkv, cap_out), dev)
+        io = _tensor(index, "index", torch.int32, (B, Hkv, keep), dev)
+        lo = _tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+        _done(ssa_cache_evict(kp, vp, mp, lp, ko, vo, mo, io, lo, B, Hkv, cap, cap_out, d, keep, sink, recent, st),
+              "ssa_cache_evict")
+    return Evicted(k_out, v_out, mass_out, index, new_lens)
