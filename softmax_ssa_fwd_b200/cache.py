@@ -55,43 +55,58 @@ def _need(ok: bool, what: str) -> None:
         raise SSAError(SSA_ERR_INVALID_ARG, what)
 
 
-def _tensor(t, name, dtype, shape, device, contiguous=True):
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == device
-          and (not contiguous or t.is_contiguous()),
-          f"{name}: want {'contiguous ' if contiguous else ''}{dtype} {tuple(shape)} on {device}")
+def _refuse(name, dtype, shape, dev, contiguous=True):
+    raise SSAError(SSA_ERR_INVALID_ARG, f"{name}: want {'contiguous ' if contiguous else ''}{dtype} {tuple(shape)} on "
+                                        + ("the CPU" if dev < 0 else f"cuda:{dev}"))
+
+
+# (The checks run on every call and cost as much as a small kernel: no text is put together unless one fails.)
+def _tensor(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type and shape on device number ``dev`` (-1: the CPU)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _refuse(name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _tensor(t, name, dtype, shape, device)
+def _optional(t, name, dtype, shape, dev):
+    return None if t is None else _tensor(t, name, dtype, shape, dev)
 
 
 def _heads(x, name):
-    _need(isinstance(x, torch.Tensor) and x.dim() == 4 and x.dtype == torch.bfloat16 and x.is_cuda,
-          f"{name}: want a 4-dimensional bf16 CUDA tensor")
+    if not (isinstance(x, torch.Tensor) and x.dim() == 4 and x.dtype is torch.bfloat16 and x.is_cuda):
+        raise SSAError(SSA_ERR_INVALID_ARG, f"{name}: want a 4-dimensional bf16 CUDA tensor")
     return x.shape
 
 
-class _On:
-    """The device of a call made current, and its stream (torch's allocations inside follow it)."""
+def _strided(x, name, shape, dev):
+    """The batch, token and head stride of a tensor whose heads' columns are contiguous."""
+    s = x.stride() if isinstance(x, torch.Tensor) else ()
+    if not (x.dtype is torch.bfloat16 and x.shape == shape and x.get_device() == dev and s[3] == 1):
+        _refuse(name + " (columns of a head contiguous)", torch.bfloat16, shape, dev, contiguous=False)
+    return s[:3]
 
-    def __init__(self, device, stream):
-        self.stack = contextlib.ExitStack()
-        if torch.cuda.current_device() != device.index:
-            self.stack.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            _need(stream.device == device, "stream: belongs to another device than the tensors")
-            self.stack.enter_context(torch.cuda.stream(stream))
-        self.device = device
+
+class _On:
+    """Makes the device of a call current, and a stream that the caller named; torch's allocations inside follow it."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stack = dev, None
+        if stream is not None or torch.cuda.current_device() != dev:
+            self.stack = contextlib.ExitStack()
+            self.stack.enter_context(torch.cuda.device(dev))
+            if stream is not None:
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
+                _need(stream.device.index == dev, "stream: belongs to another device than the tensors")
+                self.stack.enter_context(torch.cuda.stream(stream))
 
     def __enter__(self):
-        self.stack.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *e):
-        return self.stack.__exit__(*e)
+        if self.stack is not None:
+            self.stack.__exit__(*e)
 
 
 def _done(status, what):
@@ -145,27 +160,26 @@ def append(q, k, v, k_cache, v_cache, positions=None, *, inv_freq=None, axis=Non
     without ``out`` they are undefined.
     """
     B, L, Hq, d = _heads(q, "q")
-    dev = q.device
+    dev = q.get_device()
     Hkv = _heads(k, "k")[2]
-    _tensor(k, "k", torch.bfloat16, (B, L, Hkv, d), dev, contiguous=False)
-    _tensor(v, "v", torch.bfloat16, (B, L, Hkv, d), dev, contiguous=False)
-    _need(all(x.stride(3) == 1 for x in (q, k, v)), "q, k, v: the columns of a head have to be contiguous")
+    kv = (B, L, Hkv, d)
+    strides = (ctypes.c_int64 * 9)(*_strided(q, "q", q.shape, dev), *_strided(k, "k", kv, dev),
+                                   *_strided(v, "v", kv, dev))
     cap = _heads(k_cache, "k_cache")[1]
     kc = _tensor(k_cache, "k_cache", torch.bfloat16, (B, cap, Hkv, d), dev)
     vc = _tensor(v_cache, "v_cache", torch.bfloat16, (B, cap, Hkv, d), dev)
     rot, axes, freq, ax, pos = 0, 1, None, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        freq = _tensor(inv_freq, "inv_freq", torch.float64, (rot // 2,), torch.device("cpu"))
+        freq = _tensor(inv_freq, "inv_freq", torch.float64, (rot // 2,), -1)
         _need(isinstance(positions, torch.Tensor) and positions.dim() in (2, 3), "positions: want [B, L] or [B, L, axes]")
         axes = positions.shape[2] if positions.dim() == 3 else 1
         pos = _tensor(positions, "positions", torch.int32, (B, L, axes) if positions.dim() == 3 else (B, L), dev)
-        ax = _optional(axis, "axis", torch.int32, (rot // 2,), torch.device("cpu"))
+        ax = _optional(axis, "axis", torch.int32, (rot // 2,), -1)
     wq = _optional(q_weight, "q_weight", torch.float32, (d,), dev)
     wk = _optional(k_weight, "k_weight", torch.float32, (d,), dev)
     s0 = _optional(start, "start", torch.int32, (B,), dev)
     cnt = _optional(count, "count", torch.int32, (B,), dev)
-    strides = (ctypes.c_int64 * 9)(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(B, L, Hq, d, dtype=torch.bfloat16, device=dev)
@@ -184,7 +198,7 @@ def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, wor
     lse [B, Hq, T] fp32).  ``workspace``: uint8, ``ssa_decode_tree_workspace_bytes`` bytes.
     """
     B, T, Hq, d = _heads(q, "q")
-    dev = q.device
+    dev = q.get_device()
     _, cap, Hkv, _ = _heads(k, "k")
     qp = _tensor(q, "q", torch.bfloat16, q.shape, dev)
     kp = _tensor(k, "k", torch.bfloat16, (B, cap, Hkv, d), dev)
@@ -203,7 +217,8 @@ def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, wor
         if workspace is None:
             workspace = torch.empty(max(16, ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d)), dtype=torch.uint8,
                                     device=dev)
-        _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: want a contiguous tensor on {dev}")
+        if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
+            raise SSAError(SSA_ERR_INVALID_ARG, f"workspace: want a contiguous tensor on cuda:{dev}")
         op = _tensor(out, "out", torch.bfloat16, (B, T, Hq, d), dev)
         sp = _tensor(lse, "lse", torch.float32, (B, Hq, T), dev)
         _done(ssa_decode_tree(qp, kp, vp, op, sp, lp, mp, B, T, Hq, Hkv, cap, d, scale, workspace.data_ptr(),
@@ -217,7 +232,7 @@ def attn_mass(q, k, lse, *, lens=None, causal=True, scale=None, window=0, mass=N
     the query heads of a key head.  Returns mass [B, Hkv, cap] fp32 (``out``; may be ``mass`` itself), 0 past lens[b].
     """
     B, Lq, Hq, d = _heads(q, "q")
-    dev = q.device
+    dev = q.get_device()
     _, cap, Hkv, _ = _heads(k, "k")
     qp = _tensor(q, "q", torch.bfloat16, q.shape, dev)
     kp = _tensor(k, "k", torch.bfloat16, (B, cap, Hkv, d), dev)
@@ -251,7 +266,7 @@ def evict(k, v, mass, lens, *, keep, sink=0, recent=0, k_out=None, v_out=None, m
     Returns ``Evicted``.
     """
     B, cap, Hkv, d = _heads(k, "k")
-    dev = k.device
+    dev = k.get_device()
     kp = _tensor(k, "k", torch.bfloat16, k.shape, dev)
     vp = _tensor(v, "v", torch.bfloat16, k.shape, dev)
     mp = _tensor(mass, "mass", torch.float32, (B, Hkv, cap), dev)

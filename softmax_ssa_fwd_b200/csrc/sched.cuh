@@ -45,36 +45,35 @@ __device__ __forceinline__ void tile_prefix(int* pref, int B, Tiles tiles) {
   if (lane == 0) pref[0] = 0;
 }
 
-__device__ __forceinline__ long long range_start(long long U, int c, int C) { return U * c / C; }
+// U c / C, rounded down, in 32 bits (C <= 2^15)
+__device__ __forceinline__ int range_start(int U, int c, int C) { return U / C * c + U % C * c / C; }
 
-// Walks one block's segments in order.
+// Walks one block's segments in order.  (The units of a batch fit 32 bits: its cache fits the GPU's memory.)
 struct SegWalk {
   const int* pref;
-  int inner, b;
-  long long u, u1;
+  int inner, b, u, u1;
   __device__ __forceinline__ SegWalk(const int* pref_, int B, int inner_, int c, int C) : pref(pref_), inner(inner_) {
-    const long long U = (long long)inner * pref[B];
-    if (C > U) C = (int)U;
+    const int U = inner * pref[B];
+    if (C > U) C = U;
     u = c < C ? range_start(U, c, C) : U;
     u1 = c < C ? range_start(U, c + 1, C) : U;
     int lo = 0, hi = B - 1;  // the sequence that holds unit u
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)inner * pref[mid + 1] > u) hi = mid;
+      if (inner * pref[mid + 1] > u) hi = mid;
       else lo = mid + 1;
     }
     b = lo;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (u >= u1) return false;
-    while ((long long)inner * pref[b + 1] <= u) ++b;  // u < u1 <= U: some sequence holds it
+    while (inner * pref[b + 1] <= u) ++b;  // u < u1 <= U: some sequence holds it
     s.b = b;
     s.tiles = pref[b + 1] - pref[b];
-    const long long off = u - (long long)inner * pref[b];
-    s.in = (int)(off / s.tiles);
-    s.kt0 = (int)(off % s.tiles);
-    const long long left = u1 - u;
-    s.nt = (int)(left < s.tiles - s.kt0 ? left : s.tiles - s.kt0);
+    const int off = u - inner * pref[b];
+    s.in = off / s.tiles;
+    s.kt0 = off - s.in * s.tiles;
+    s.nt = min(u1 - u, s.tiles - s.kt0);
     u += s.nt;
     return true;
   }
@@ -87,17 +86,20 @@ struct Waiter {
   int* status;
   unsigned long long limit_ns;
   __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
+    // Counted in clocks, two a nanosecond, more than the SM makes.  An attempt sleeps for as long as the hardware
+    // likes, so a wait that has outlasted the limit gives up even where its attempt succeeded.
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    if (mbar_test_wait(a, parity)) return true;
+    const unsigned long long t0 = clock64();
     for (;;) {
-      if (mbar_try_wait(a, parity)) return true;
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
+      const bool there = mbar_try_wait(a, parity);
+      if (clock64() - t0 > 2 * limit_ns) {
         *abort = 1;
         atomicOr(status, 1);
         return false;
       }
+      if (there) return true;
+      if (*abort) return false;
     }
   }
 };

@@ -192,15 +192,17 @@ __global__ void __launch_bounds__(NT, 1)
         ssa::mbar_wait(smem_u32(&kfull[t % KST]), (t / KST) & 1, DRAIN_NS);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
+      const uint32_t leader = ssa::elect_one();
+      auto waits = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       constexpr uint32_t idesc = ssa::idesc_bf16_f32(BK, N, false, false);
       int g = 0, n = 0;
       bool ok = true;
       while (ok && walk.next(s)) {
-        ok = wait(&q_full, n & 1);
+        ok = waits(&q_full, n & 1);
         for (int t = 0; ok && t < s.nt; ++t, ++g) {
           const int st = g % KST;
-          if (!wait(&kfull[st], (g / KST) & 1) || !wait(&s_empty[g & 1], ((g >> 1) & 1) ^ 1)) {
+          if (!waits(&kfull[st], (g / KST) & 1) || !waits(&s_empty[g & 1], ((g >> 1) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -208,17 +210,17 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
           for (int k16 = 0; k16 < D / 16; ++k16) {
             const uint32_t in = (k16 & 3) * 32;
-            ssa::mma_ss(tmem + 256 * (g & 1),
+            ssa::mma_ss_warp(leader, tmem + 256 * (g & 1),
                         ssa::smem_desc_sw128(k_s + st * L::K_BYTES + (k16 >> 2) * BK * 128 + in, 16, 1024),
                         ssa::smem_desc_sw128(q_s + (k16 >> 2) * N * 128 + in, 16, 1024), idesc, k16 > 0);
           }
-          ssa::mma_commit(smem_u32(&s_full[g & 1]));
-          ssa::mma_commit(smem_u32(&kempty[st]));
+          ssa::mma_commit_warp(leader, smem_u32(&s_full[g & 1]));
+          ssa::mma_commit_warp(leader, smem_u32(&kempty[st]));
         }
-        if (ok) ssa::mma_commit(smem_u32(&q_empty));
+        if (ok) ssa::mma_commit_warp(leader, smem_u32(&q_empty));
         ++n;
       }
-      ssa::mma_commit(smem_u32(&done));
+      ssa::mma_commit_warp(leader, smem_u32(&done));
       ssa::mbar_wait(smem_u32(&done), 0, DRAIN_NS);  // no MMA in flight when TMEM is freed
     }
   } else if (warp == 2) {
@@ -399,23 +401,25 @@ __global__ void __launch_bounds__(NT, 1)
         ssa::mbar_wait(smem_u32(&qfull[t % QST]), (t / QST) & 1, DRAIN_NS);
     }
   } else if (warp == 1) {
-    if (lane == 0 && t0 < t1) {
+    if (t0 < t1) {
+      const uint32_t leader = ssa::elect_one();
+      auto waits = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       constexpr uint32_t idesc = ssa::idesc_bf16_f32(BK, BN, false, false);
-      bool ok = wait(&k_full, 0);
+      bool ok = waits(&k_full, 0);
       for (int g = 0; ok && g < t1 - t0; ++g) {
         const int st = g % QST, buf = g % NBUF;
-        if (!wait(&qfull[st], (g / QST) & 1) || !wait(&s_empty[buf], ((g / NBUF) & 1) ^ 1)) break;
+        if (!waits(&qfull[st], (g / QST) & 1) || !waits(&s_empty[buf], ((g / NBUF) & 1) ^ 1)) break;
         ssa::tc_fence_after();
 #pragma unroll
         for (int k16 = 0; k16 < D / 16; ++k16) {
           const uint32_t o = (k16 >> 2) * 128 * 128 + (k16 & 3) * 32;
-          ssa::mma_ss(tmem + 128 * buf, ssa::smem_desc_sw128(k_s + o, 16, 1024),
+          ssa::mma_ss_warp(leader, tmem + 128 * buf, ssa::smem_desc_sw128(k_s + o, 16, 1024),
                       ssa::smem_desc_sw128(q_s + st * L::Q_BYTES + o, 16, 1024), idesc, k16 > 0);
         }
-        ssa::mma_commit(smem_u32(&s_full[buf]));
-        ssa::mma_commit(smem_u32(&qempty[st]));
+        ssa::mma_commit_warp(leader, smem_u32(&s_full[buf]));
+        ssa::mma_commit_warp(leader, smem_u32(&qempty[st]));
       }
-      ssa::mma_commit(smem_u32(&done));
+      ssa::mma_commit_warp(leader, smem_u32(&done));
       ssa::mbar_wait(smem_u32(&done), 0, DRAIN_NS);
     }
   } else if (warp < 4) {
