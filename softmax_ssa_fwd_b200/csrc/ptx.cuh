@@ -360,6 +360,24 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// v[r] of every lane combined over the warp's lanes, r = lane % N, for N values
+// in N - 1 + log2(32 / N) shuffles: each step halves the values a lane keeps.
+template <int N, class Op>
+__device__ __forceinline__ float reduce_across(float* v, Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1 (sm_100).
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo_bytes,
                                                     uint32_t sbo_bytes) {

@@ -2,18 +2,18 @@
 // (ssa_attn_mass) on B200 (sm_100a).
 //
 // Given the rows' log-sum-exp, the weight of key j is a sum over query rows of
-// exp(scale q.k_j - lse).  Both kernels compute S^T = K Q^T on tcgen05 with the
-// 128 keys of a tile on the M side, so that a TMEM lane is a key: one thread owns
-// a key and adds its row's exponentials in registers, with no reduction between
-// threads, no atomics and no probabilities written anywhere.  Query rows are
-// packed token-major over the G query heads of a key head (row i * G + g).
+// exp(scale q.k_j - lse).  The scores are computed on tcgen05 and summed without
+// atomics and without writing a probability anywhere.  Query rows are packed
+// token-major over the G query heads of a key head (row i * G + g).
 //
-//   stream kernel: all G * window rows fit one operand tile (<= 256 rows).  The
-//     rows stay in shared memory and the key tiles stream past, each read
-//     once: bound by HBM (2 * d bytes a key and key head).
-//   prompt kernel: more rows.  A key tile stays and the row tiles stream past
-//     from L2: bound by the exponentials (MUFU, 16 a clock and SM: 1,024
-//     clocks a 128 x 128 tile against 512 for its matrix product).
+//   stream kernel: all G * window rows fit one operand (<= 256 rows).  S^T = K Q^T,
+//     a thread a key, which adds its row's exponentials; the rows stay in
+//     shared memory and the key tiles stream past, each read once: bound by
+//     HBM (2 * d bytes a key and key head) up to about 64 rows, then by the
+//     exponentials (16 a clock and SM).
+//   prompt kernel: more rows.  Keys stay and the row tiles stream past from L2:
+//     bound by the exponentials, 1,024 clocks a 128 x 128 tile against 512 for
+//     its matrix product.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -39,7 +39,7 @@ using ssa::SegWalk;
 using ssa::smem_u32;
 
 constexpr int BK = 128;  // keys per tile: the M of the MMA
-constexpr int NT = 384;  // warp 0 producer, 1 MMA, 2 rows and lse, 3 zero fill, 4-11 sums
+constexpr int NT = 640;  // warp 0 producer, 1 MMA, 2 rows and lse, 3 zero fill, 4-19 sums, in four groups
 constexpr unsigned long long DRAIN_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -71,6 +71,12 @@ __device__ __forceinline__ float neg_lse2(const Params& p, int b, int hkv, int r
   return l == -INFINITY ? -INFINITY : -l * LOG2E;
 }
 
+template <int NC>
+__device__ __forceinline__ void load_columns(uint32_t taddr, float* x) {
+  if constexpr (NC == 16) ssa::tmem_ld16f(taddr, x);
+  else ssa::tmem_ld32f(taddr, x);
+}
+
 // Adds exp2(s c + nl) over NC columns; columns below `first` do not count.
 template <int NC, bool MASK>
 __device__ __forceinline__ void add_columns(const float* x, const float* nl, float c, int first, uint64_t (&acc)[2]) {
@@ -93,6 +99,21 @@ __device__ __forceinline__ void add_columns(const float* x, const float* nl, flo
     }
   }
 }
+// The same over NC columns of S^T at `at`, 32 (16) at a time; `after` runs once they are in registers.
+template <int NC, class After>
+__device__ __forceinline__ void add_tile(uint32_t at, const float* nl, float c, bool mask, int first, uint64_t (&acc)[2],
+                                         After after) {
+  constexpr int CH = NC < 32 ? NC : 32;
+#pragma unroll
+  for (int i = 0; i < NC; i += CH) {
+    float x[CH];
+    load_columns<CH>(at + i, x);
+    ssa::tmem_wait_ld();
+    if (i + CH == NC) after();
+    if (mask) add_columns<CH, true>(x, nl + i, c, first - i, acc);
+    else add_columns<CH, false>(x, nl + i, c, 0, acc);
+  }
+}
 __device__ __forceinline__ float total(const uint64_t (&acc)[2]) {
   float a, b, c, d;
   ssa::f2_unpack(acc[0], a, b);
@@ -100,17 +121,12 @@ __device__ __forceinline__ float total(const uint64_t (&acc)[2]) {
   return (a + b) + (c + d);
 }
 
-template <int NC>
-__device__ __forceinline__ void load_columns(uint32_t taddr, float* x) {
-  if constexpr (NC == 16) ssa::tmem_ld16f(taddr, x);
-  else if constexpr (NC == 32) ssa::tmem_ld32f(taddr, x);
-  else ssa::tmem_ld64f(taddr, x);
-}
-
 // ============================================================ stream kernel
 
 template <int D, int N>
 struct StreamSmem {
+  static constexpr int NB = N <= 128 ? 4 : 2;  // S^T buffers; a group per tile, or two that halve its columns
+  static constexpr int NC = N / (4 / NB);      // columns of a group
   static constexpr uint32_t Q_BYTES = N * D * 2;
   static constexpr uint32_t K_BYTES = BK * D * 2;
   static constexpr int FIT = (int)((208 * 1024 - Q_BYTES) / K_BYTES);
@@ -123,11 +139,13 @@ __global__ void __launch_bounds__(NT, 1)
     mass_stream_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ Params p) {
   using L = StreamSmem<D, N>;
-  constexpr int KST = L::KST;
-  constexpr int NC = N < 64 ? N : 64;  // columns per TMEM load
+  constexpr int KST = L::KST, NB = L::NB, NC = L::NC;
+  constexpr bool HALVES = NB == 2;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t kfull[KST], kempty[KST], q_full, q_empty, lse_full[2], lse_empty[2], s_full[2], s_empty[2], done;
+  __shared__ uint64_t kfull[KST], kempty[KST], q_full, q_empty, lse_full[2], lse_empty[2], s_full[NB], s_empty[NB], done;
+  __shared__ uint64_t half_full[2], half_empty[2];
+  __shared__ float half_sum[2][BK];
   __shared__ __align__(16) float nlse[2][N];
   __shared__ int pref[ssa::MAX_SEQS + 1];
   __shared__ uint32_t tmem_base;
@@ -145,9 +163,13 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(smem_u32(&done), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&lse_full[i]), 32);
-      mbar_init(smem_u32(&lse_empty[i]), 8);
+      mbar_init(smem_u32(&lse_empty[i]), 16);
+      mbar_init(smem_u32(&half_full[i]), 4);
+      mbar_init(smem_u32(&half_empty[i]), 4);
+    }
+    for (int i = 0; i < NB; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_empty[i]), 4);
+      mbar_init(smem_u32(&s_empty[i]), HALVES ? 8 : 4);
     }
     abort_flag = 0;
     ssa::fence_mbar_init();
@@ -202,7 +224,7 @@ __global__ void __launch_bounds__(NT, 1)
         ok = waits(&q_full, n & 1);
         for (int t = 0; ok && t < s.nt; ++t, ++g) {
           const int st = g % KST;
-          if (!waits(&kfull[st], (g / KST) & 1) || !waits(&s_empty[g & 1], ((g >> 1) & 1) ^ 1)) {
+          if (!waits(&kfull[st], (g / KST) & 1) || !waits(&s_empty[g % NB], ((g / NB) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -210,11 +232,11 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
           for (int k16 = 0; k16 < D / 16; ++k16) {
             const uint32_t in = (k16 & 3) * 32;
-            ssa::mma_ss_warp(leader, tmem + 256 * (g & 1),
+            ssa::mma_ss_warp(leader, tmem + 512 / NB * (g % NB),
                         ssa::smem_desc_sw128(k_s + st * L::K_BYTES + (k16 >> 2) * BK * 128 + in, 16, 1024),
                         ssa::smem_desc_sw128(q_s + (k16 >> 2) * N * 128 + in, 16, 1024), idesc, k16 > 0);
           }
-          ssa::mma_commit_warp(leader, smem_u32(&s_full[g & 1]));
+          ssa::mma_commit_warp(leader, smem_u32(&s_full[g % NB]));
           ssa::mma_commit_warp(leader, smem_u32(&kempty[st]));
         }
         if (ok) ssa::mma_commit_warp(leader, smem_u32(&q_empty));
@@ -247,8 +269,9 @@ __global__ void __launch_bounds__(NT, 1)
       for (int j = (n + BK - 1) / BK * BK + lane; j < p.cap; j += 32) p.mass_out[(size_t)x * p.cap + j] = 0.f;
     }
   } else {
-    const int wg = (warp - 4) >> 2;  // tiles wg, wg + 2, ...
-    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * wg;
+    // group gr: tiles gr, gr + 4, ...; with halves tiles gr & 1, + 2, ..., columns of half gr >> 1
+    const int gr = (warp - 4) >> 2, buf = gr % NB, half = HALVES ? gr >> 1 : 0;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 512 / NB * buf + NC * half;
     const int row = (warp & 3) * 32 + lane;
     int g = 0, n = 0;
     bool ok = true;
@@ -257,30 +280,31 @@ __global__ void __launch_bounds__(NT, 1)
       const size_t out = ((size_t)s.b * p.Hkv + s.in) * p.cap;
       ok = __all_sync(0xffffffffu, wait(&lse_full[n & 1], (n >> 1) & 1));
       for (int t = 0; ok && t < s.nt; ++t, ++g) {
-        if ((g & 1) != wg) continue;
+        if (g % NB != buf) continue;
         const int j0 = (s.kt0 + t) * BK, j = j0 + row;
-        const float before = p.mass_in != nullptr && j < len ? p.decay * p.mass_in[out + j] : 0.f;
-        ok = __all_sync(0xffffffffu, wait(&s_full[wg], (g >> 1) & 1));
+        const float before = half == 0 && p.mass_in != nullptr && j < len ? p.decay * p.mass_in[out + j] : 0.f;
+        ok = __all_sync(0xffffffffu, wait(&s_full[buf], (g / NB) & 1));
         if (!ok) break;
         ssa::tc_fence_after();
         // row i of the window sits at i + len - W: key j counts from there on
         const bool mask = p.causal && j0 + BK - 1 > len - p.W;
-        const int first = mask ? (j - len + p.W) * p.G : 0;
         uint64_t acc[2] = {ssa::f2_pack(0.f, 0.f), ssa::f2_pack(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < N / NC; ++c) {
-          float x[NC];
-          load_columns<NC>(lanes + c * NC, x);
-          ssa::tmem_wait_ld();
-          if (c == N / NC - 1) {  // S is in registers: the buffer is free
-            ssa::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_empty[wg]));
-          }
-          if (mask) add_columns<NC, true>(x, &nlse[n & 1][c * NC], p.c, first - c * NC, acc);
-          else add_columns<NC, false>(x, &nlse[n & 1][c * NC], p.c, 0, acc);
+        add_tile<NC>(lanes, &nlse[n & 1][NC * half], p.c, mask, (j - len + p.W) * p.G - NC * half, acc, [&] {
+          ssa::tc_fence_before();  // S is in registers: the buffer is free
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
+        });
+        float sum = total(acc);
+        if (HALVES) {  // the second half's sum goes to the first half's group
+          const uint32_t parity = (g / NB) & 1;
+          ok = __all_sync(0xffffffffu, half == 1 ? wait(&half_empty[buf], parity ^ 1) : wait(&half_full[buf], parity));
+          if (!ok) break;
+          if (half == 1) half_sum[buf][row] = sum;
+          else sum += half_sum[buf][row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(half == 1 ? &half_full[buf] : &half_empty[buf]));
         }
-        if (j < p.cap) p.mass_out[out + j] = j < len ? before + total(acc) : 0.f;
+        if (half == 0 && j < p.cap) p.mass_out[out + j] = j < len ? before + sum : 0.f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&lse_empty[n & 1]));
@@ -298,55 +322,64 @@ __global__ void __launch_bounds__(NT, 1)
 // ============================================================ prompt kernel
 
 constexpr int BN = 128;   // rows per row tile
-constexpr int NLSE = 8;   // row tiles whose lse is in shared memory
-constexpr int NBUF = 4;   // S^T buffers in TMEM
+constexpr int KB = 256;   // keys of a block
+constexpr int NTP = 576;  // warp 0 producer, 1 MMA, 2-17 sums: 16 warps at 112 registers
 
 template <int D>
 struct PromptSmem {
-  static constexpr uint32_t K_BYTES = BK * D * 2;
+  static constexpr uint32_t K_BYTES = KB * D * 2;
   static constexpr uint32_t Q_BYTES = BN * D * 2;
-  static constexpr int QST = D == 128 ? 5 : 8;
+  static constexpr int QST = D == 128 ? 4 : 8;
   static constexpr uint32_t TOTAL = 1024 + K_BYTES + QST * Q_BYTES;
 };
 
-// Block (cluster rank r of S): key tile kt of one (sequence, key head), every
-// S-th part of the row tiles that see it; the parts are added through
-// distributed shared memory in rank order.
+// Block (cluster rank r of S): 256 keys of one (sequence, key head) and the r-th
+// S-th of the row tiles that see them; the parts are added through distributed
+// shared memory in rank order.  S = Q K^T, a thread a row and 64 of the keys:
+// its lse is one register and its 64 sums stay in registers over all row
+// tiles, added over the threads once at the end.  (A thread a key, as in the
+// stream kernel, reads a lse from shared memory for every exponential, which
+// goes through the same queue as they do: 340 us against 4 % below the figure
+// of this form at 8,192 rows and keys of 32 / 8 heads.)  256 keys, because every
+// row tile comes from L2, 32 KB (d = 128) in the 2,048 clocks of its exponentials.
 template <int D>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(NTP, 1)
     mass_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ Params p) {
   using L = PromptSmem<D>;
   constexpr int QST = L::QST;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t k_full, qfull[QST], qempty[QST], lse_full[NLSE], lse_empty[NLSE], s_full[NBUF], s_empty[NBUF], done;
-  __shared__ __align__(16) float nlse[NLSE][BN];
-  __shared__ float part[2][BK];
+  __shared__ uint64_t k_full, qfull[QST], qempty[QST], s_full[2], s_empty[2], done;
+  __shared__ float quad_sum[4][KB], part[KB];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // low key tiles first: under a causal mask they are seen by the most rows
+  // low keys first: under a causal mask they are seen by the most rows
   const int item = blockIdx.x / S, pairs = p.B * p.Hkv;
   const int kt = item / pairs, pair = item % pairs;
   const int b = pair / p.Hkv, hkv = pair % p.Hkv;
   const int len = clamp_len(p.lens, b, p.cap);
-  const int j0 = kt * BK;
+  const int j0 = kt * KB;
   float* out = p.mass_out + (size_t)pair * p.cap;
   const float* in = p.mass_in != nullptr ? p.mass_in + (size_t)pair * p.cap : nullptr;
   if (j0 >= len) {  // the same for every block of the cluster
-    if (rank == 0 && tid < BK && j0 + tid < p.cap) out[j0 + tid] = 0.f;
+    if (rank == 0 && tid < KB && j0 + tid < p.cap) out[j0 + tid] = 0.f;
     return;
   }
-  // first row tile that sees the tile's first key, and this rank's range
+  // first row tile that sees the block's first key, and this rank's range
   const int t_first = p.causal ? min(max((j0 - len + p.W) / p.tok, 0), p.tiles) : 0;
   const int nt = p.tiles - t_first;
   const int t0 = t_first + (int)((long long)nt * rank / S), t1 = t_first + (int)((long long)nt * (rank + 1) / S);
   const uint32_t k_s = smem_u32(base), q_s = k_s + L::K_BYTES;
 
+  if (tid == 32) {
+    ssa::tma_prefetch_desc(&tm_q);
+    ssa::tma_prefetch_desc(&tm_k);
+  }
   if (tid == 0) {
     mbar_init(smem_u32(&k_full), 1);
     mbar_init(smem_u32(&done), 1);
@@ -354,13 +387,9 @@ __global__ void __launch_bounds__(NT, 1)
       mbar_init(smem_u32(&qfull[i]), 1);
       mbar_init(smem_u32(&qempty[i]), 1);
     }
-    for (int i = 0; i < NLSE; ++i) {
-      mbar_init(smem_u32(&lse_full[i]), 64);
-      mbar_init(smem_u32(&lse_empty[i]), 4);
-    }
-    for (int i = 0; i < NBUF; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_empty[i]), 4);
+      mbar_init(smem_u32(&s_empty[i]), 16);
     }
     abort_flag = 0;
     ssa::fence_mbar_init();
@@ -369,11 +398,6 @@ __global__ void __launch_bounds__(NT, 1)
     ssa::tmem_alloc(smem_u32(&tmem_base), 512);
     ssa::tmem_relinquish();
   }
-  if (p.G * p.tok < BN) {  // operand rows past the tile's tokens are never loaded: zero
-    for (int e = tid; e < (int)(QST * L::Q_BYTES / 16); e += NT)
-      reinterpret_cast<uint4*>(base + L::K_BYTES)[e] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  ssa::fence_proxy_async_smem();
   ssa::tc_fence_before();
   __syncthreads();
   ssa::tc_fence_after();
@@ -384,8 +408,10 @@ __global__ void __launch_bounds__(NT, 1)
     if (lane == 0 && t0 < t1) {
       mbar_arrive_expect_tx(smem_u32(&k_full), L::K_BYTES);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        ssa::tma_load_4d(k_s + c * BK * 128, &tm_k, smem_u32(&k_full), c * 64, hkv, j0, b);
+      for (int x = 0; x < KB / BK; ++x)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          ssa::tma_load_4d(k_s + (c * KB + x * BK) * 128, &tm_k, smem_u32(&k_full), c * 64, hkv, j0 + x * BK, b);
       int g = 0;
       for (int t = t0; t < t1; ++t, ++g) {
         const int st = g % QST;
@@ -404,60 +430,81 @@ __global__ void __launch_bounds__(NT, 1)
     if (t0 < t1) {
       const uint32_t leader = ssa::elect_one();
       auto waits = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-      constexpr uint32_t idesc = ssa::idesc_bf16_f32(BK, BN, false, false);
-      bool ok = waits(&k_full, 0);
+      constexpr uint32_t idesc = ssa::idesc_bf16_f32(BN, KB, false, false);
+      const bool ok = waits(&k_full, 0);
       for (int g = 0; ok && g < t1 - t0; ++g) {
-        const int st = g % QST, buf = g % NBUF;
-        if (!waits(&qfull[st], (g / QST) & 1) || !waits(&s_empty[buf], ((g / NBUF) & 1) ^ 1)) break;
+        const int st = g % QST;
+        if (!waits(&qfull[st], (g / QST) & 1) || !waits(&s_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
         ssa::tc_fence_after();
 #pragma unroll
-        for (int k16 = 0; k16 < D / 16; ++k16) {
-          const uint32_t o = (k16 >> 2) * 128 * 128 + (k16 & 3) * 32;
-          ssa::mma_ss_warp(leader, tmem + 128 * buf, ssa::smem_desc_sw128(k_s + o, 16, 1024),
-                      ssa::smem_desc_sw128(q_s + st * L::Q_BYTES + o, 16, 1024), idesc, k16 > 0);
-        }
-        ssa::mma_commit_warp(leader, smem_u32(&s_full[buf]));
+        for (int k16 = 0; k16 < D / 16; ++k16)
+          ssa::mma_ss_warp(leader, tmem + KB * (g & 1),
+                           ssa::smem_desc_sw128(q_s + st * L::Q_BYTES + (k16 >> 2) * BN * 128 + (k16 & 3) * 32, 16, 1024),
+                           ssa::smem_desc_sw128(k_s + (k16 >> 2) * KB * 128 + (k16 & 3) * 32, 16, 1024), idesc, k16 > 0);
+        ssa::mma_commit_warp(leader, smem_u32(&s_full[g & 1]));
         ssa::mma_commit_warp(leader, smem_u32(&qempty[st]));
       }
       ssa::mma_commit_warp(leader, smem_u32(&done));
       ssa::mbar_wait(smem_u32(&done), 0, DRAIN_NS);
     }
-  } else if (warp < 4) {
-    const int t64 = tid - 64;
-    for (int g = 0; g < t1 - t0; ++g) {
-      const int sl = g % NLSE;
-      if (!__all_sync(0xffffffffu, wait(&lse_empty[sl], ((g / NLSE) & 1) ^ 1))) break;
-      for (int r = t64; r < BN; r += 64)
-        nlse[sl][r] = r < p.G * p.tok ? neg_lse2(p, b, hkv, (t0 + g) * p.tok * p.G + r) : -INFINITY;
-      mbar_arrive(smem_u32(&lse_full[sl]));
-    }
   } else {
-    const int wg = (warp - 4) >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int row = (warp & 3) * 32 + lane, j = j0 + row;
-    float sum = 0.f;
-    for (int g = wg; g < t1 - t0; g += 2) {
-      const int buf = g % NBUF, sl = g % NLSE;
-      if (!__all_sync(0xffffffffu, wait(&lse_full[sl], (g / NLSE) & 1) && wait(&s_full[buf], (g / NBUF) & 1))) break;
+    const int slice = (warp - 2) >> 2, qd = warp & 3, row = qd * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(32 * qd) << 16) + 64 * slice;
+    const int ti = row / p.G;  // the row's token in its tile (p.tok: none)
+    const float* lse = p.lse + ((size_t)b * p.Hq + hkv * p.G + row % p.G) * p.Lq;
+    // -lse in log2 units; -inf for a row that is not there or has no keys
+    auto neg_lse = [&](int g) {
+      const int i = p.Lq - p.W + (t0 + g) * p.tok + ti;
+      const float l = g < t1 - t0 && ti < p.tok && i < p.Lq ? lse[i] : -INFINITY;
+      return l == -INFINITY ? -INFINITY : -l * LOG2E;
+    };
+    const uint64_t c2 = ssa::f2_pack(p.c, p.c);
+    uint64_t acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = ssa::f2_pack(0.f, 0.f);
+    float next = neg_lse(0);
+#pragma unroll 1
+    for (int g = 0; g < t1 - t0; ++g) {
+      const float nl = next;
+      next = neg_lse(g + 1);
+      // keys of the slice that the row sees: the first `sees`; a row without lse none
+      int sees = 64;
+      if (p.causal) sees = min((t0 + g) * p.tok + ti + len - p.W - (j0 + 64 * slice) + 1, 64);
+      if (nl == -INFINITY) sees = 0;
+      const bool mask = __any_sync(0xffffffffu, sees < 64);
+      if (!__all_sync(0xffffffffu, wait(&s_full[g & 1], (g >> 1) & 1))) break;
       ssa::tc_fence_after();
-      const int i0 = (t0 + g) * p.tok;  // the tile's first row, in the window
-      const bool mask = p.causal && j0 + BK - 1 > i0 + len - p.W;
-      const int first = mask ? (j - len + p.W - i0) * p.G : 0;
-      uint64_t acc[2] = {ssa::f2_pack(0.f, 0.f), ssa::f2_pack(0.f, 0.f)};
-      float x[BN];
-      ssa::tmem_ld64f(lanes + 128 * buf, x);
-      ssa::tmem_ld64f(lanes + 128 * buf + 64, x + 64);
-      ssa::tmem_wait_ld();
-      ssa::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
-      if (mask) add_columns<BN, true>(x, nlse[sl], p.c, first, acc);
-      else add_columns<BN, false>(x, nlse[sl], p.c, 0, acc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&lse_empty[sl]));
-      sum += total(acc);
+      const uint64_t nl2 = ssa::f2_pack(nl, nl);
+#pragma unroll
+      for (int i = 0; i < 64; i += 16) {
+        float x[16];
+        ssa::tmem_ld16f(at + KB * (g & 1) + i, x);
+        ssa::tmem_wait_ld();
+        if (i == 48) {  // S is in registers: the buffer is free
+          ssa::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[g & 1]));
+        }
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = i + e < sees ? x[e] : -INFINITY;
+        }
+        // (masked: -inf, times c > 0, plus a finite number or -inf)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          float p0, p1;
+          ssa::f2_unpack(ssa::ffma2(ssa::f2_pack(x[e], x[e + 1]), c2, nl2), p0, p1);
+          acc[(i + e) / 2] = ssa::fadd2(acc[(i + e) / 2], ssa::f2_pack(ex2(p0), ex2(p1)));
+        }
+      }
     }
-    part[wg][row] = sum;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float y[32];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) ssa::f2_unpack(acc[16 * h + e / 2], y[e], y[e + 1]);
+      quad_sum[qd][64 * slice + 32 * h + lane] = ssa::reduce_across<32>(y, [](float u, float v) { return u + v; });
+    }
   }
   ssa::tc_fence_before();
   __syncthreads();
@@ -465,12 +512,11 @@ __global__ void __launch_bounds__(NT, 1)
     ssa::tc_fence_after();
     ssa::tmem_dealloc(tmem, 512);
   }
-  if (tid < BK) part[0][tid] += part[1][tid];
+  if (tid < KB) part[tid] = (quad_sum[0][tid] + quad_sum[1][tid]) + (quad_sum[2][tid] + quad_sum[3][tid]);
   if (S > 1) cluster.sync();
-  else __syncthreads();
-  if (rank == 0 && tid < BK && j0 + tid < p.cap) {
+  if (rank == 0 && tid < KB && j0 + tid < p.cap) {
     float sum = 0.f;
-    for (int r = 0; r < S; ++r) sum += *cluster.map_shared_rank(&part[0][tid], r);
+    for (int r = 0; r < S; ++r) sum += *cluster.map_shared_rank(&part[tid], r);
     const int j = j0 + tid;
     out[j] = j < len ? (in != nullptr ? p.decay * in[j] + sum : sum) : 0.f;
   }
@@ -478,13 +524,13 @@ __global__ void __launch_bounds__(NT, 1)
 }
 
 template <class Kernel>
-static int launch(Kernel* kernel, size_t smem, long long grid, int cluster, const CUtensorMap& q, const CUtensorMap& k,
+static int launch(Kernel* kernel, int threads, size_t smem, long long grid, int cluster, const CUtensorMap& q, const CUtensorMap& k,
                   const Params& p, cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SSA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -504,7 +550,7 @@ static int run(const Params& p, const void* q, const void* k, int sms, cudaStrea
   if (R <= 256) {
     if (!ssa::tma_map_bf16_box(&mq, q, p.B, p.Lq, p.Hq, D, p.G, p.W)) return SSA_ERR_CUDA;
     const long long grid = pairs * nk < sms ? pairs * nk : sms;
-#define SSA_STREAM(N) launch(mass_stream_kernel<D, N>, StreamSmem<D, N>::TOTAL, grid, 1, mq, mk, p, st)
+#define SSA_STREAM(N) launch(mass_stream_kernel<D, N>, NT, StreamSmem<D, N>::TOTAL, grid, 1, mq, mk, p, st)
     if (R <= 16) return SSA_STREAM(16);
     if (R <= 32) return SSA_STREAM(32);
     if (R <= 64) return SSA_STREAM(64);
@@ -513,12 +559,16 @@ static int run(const Params& p, const void* q, const void* k, int sms, cudaStrea
 #undef SSA_STREAM
   }
   if (!ssa::tma_map_bf16_box(&mq, q, p.B, p.Lq, p.Hq, D, p.G, p.tok)) return SSA_ERR_CUDA;
-  // few key tiles: a cluster shares one, as long as the GPU holds them all at once
+  // A cluster shares its keys' rows until there are two blocks an SM: under a
+  // causal mask a block's rows go from all to none, and few large blocks would
+  // leave SMs idle at the end.  (No further: clusters of four leave SMs of some
+  // GPCs unused.)
+  const long long items = pairs * ((p.cap + (long long)KB - 1) / KB);
   int cs = 1;
-  while (cs < 8 && pairs * nk * cs * 2 <= sms && p.tiles >= cs * 4) cs *= 2;
-  const long long grid = pairs * nk * cs;
+  while (cs < 8 && items * cs < 2 * sms && p.tiles >= cs * 4) cs *= 2;
+  const long long grid = items * cs;
   if (grid > 0x7fffffff) return SSA_ERR_UNSUPPORTED;
-  return launch(mass_prompt_kernel<D>, PromptSmem<D>::TOTAL, grid, cs, mq, mk, p, st);
+  return launch(mass_prompt_kernel<D>, NTP, PromptSmem<D>::TOTAL, grid, cs, mq, mk, p, st);
 }
 
 }  // namespace ssa_mass

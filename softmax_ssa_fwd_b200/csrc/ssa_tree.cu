@@ -229,24 +229,6 @@ struct FewSmem {
   static constexpr uint32_t TOTAL = 1024 + Q_BYTES + (KST + VST) * KV_BYTES + P_ALL;
 };
 
-// v[r] of every lane combined over the warp's lanes, r = lane % N, for N values
-// in N - 1 + log2(32 / N) shuffles: each step halves the values a lane keeps.
-template <int N, class Op>
-__device__ __forceinline__ float reduce_across(float* v, Op op) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-    }
-  }
-#pragma unroll
-  for (int o = N; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-  return v[0];
-}
 // Whether any of the 128 threads at named barrier `id` says so.
 __device__ __forceinline__ bool any_of_group(uint32_t id, bool x) {
   uint32_t r;
@@ -480,7 +462,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
           }
           if (step == FIND) {  // (uses x up: it is read again)
-            const float top = reduce_across<N>(x, [](float u, float v) { return fmaxf(u, v); });
+            const float top = ssa::reduce_across<N>(x, [](float u, float v) { return fmaxf(u, v); });
             if (lane < N) warp_top[wg][qd][lane] = top;
             any_of_group(bar, false);
             bool empty = false;
@@ -568,7 +550,7 @@ __global__ void __launch_bounds__(NT, 1)
       float y[N];
 #pragma unroll
       for (int r = 0; r < N; r += 2) ssa::f2_unpack(l[r / 2], y[r], y[r + 1]);
-      const float part_sum = reduce_across<N>(y, [](float u, float v) { return u + v; });
+      const float part_sum = ssa::reduce_across<N>(y, [](float u, float v) { return u + v; });
       if (lane < N) sums[wg][qd][lane] = part_sum;
       if (gt < N) seg_m[n & 1][wg][gt] = any ? row_m[wg][gt] : -INFINITY;
       ssa::named_bar_sync(3, 256);
