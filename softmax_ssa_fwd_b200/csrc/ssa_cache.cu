@@ -22,9 +22,13 @@ namespace cg = cooperative_groups;
 // row (16 bytes a lane), so the angles of the token (two to eight sine/cosine
 // pairs a lane) are computed once in registers and serve all of its heads; the
 // norm is a shuffle reduction inside the row's lanes and the rotation partner,
-// half a rotated width away, comes by shuffle.
+// half a rotated width away, comes by shuffle.  The next AU head rows are on their
+// way while the current ones are computed: 75,600 tokens of 40 + 40 + 40 heads take
+// 717 us (6.5 TB/s, the rate of a copy; 1,055 without the look-ahead).  A smaller
+// register budget (spills), warps that go on to further tokens and angles shared
+// through shared memory all measured the same or slower.
 constexpr int AW = 4;  // warps per block
-constexpr int AU = 4;  // head rows a lane group has in flight
+constexpr int AU = 4;  // head rows a lane group loads at once
 
 struct AppendParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -79,90 +83,81 @@ __global__ void __launch_bounds__(32 * AW) append_kernel(const __grid_constant__
       sn[e] = s * p.factor * sign;
     }
   }
-  const int src = PAIRS || !turns ? lane : (8 * u < half ? lane + half / 8 : lane - half / 8);
-  float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wq[e] = p.wq != nullptr ? p.wq[8 * u + e] : 1.f;
-    wk[e] = p.wk != nullptr ? p.wk[8 * u + e] : 1.f;
-  }
+  const int from = PAIRS || !turns ? lane : (8 * u < half ? lane + half / 8 : lane - half / 8);
 
-  const int HT = p.Hq + 2 * p.Hkv;
-  const int h_end = min(HT, (chunk + 1) * p.per);
-  for (int h0 = chunk * p.per; h0 < h_end; h0 += RP * AU) {
-    uint4 raw[AU];
+  // Head rows [h0, h1) of one tensor: src and dst at this lane's columns of head 0.
+  auto rows = [&](int h0, int h1, const __nv_bfloat16* src, int64_t step, __nv_bfloat16* dst, const float* w, bool plain) {
+    if (h0 >= h1) return;
+    float wt[8];
+    if (w != nullptr) {
+      const float4 a = reinterpret_cast<const float4*>(w + 8 * u)[0], c = reinterpret_cast<const float4*>(w + 8 * u)[1];
+      wt[0] = a.x, wt[1] = a.y, wt[2] = a.z, wt[3] = a.w, wt[4] = c.x, wt[5] = c.y, wt[6] = c.z, wt[7] = c.w;
+    }
+    uint4 next[AU];
+    auto load = [&](int h) {
 #pragma unroll
-    for (int a = 0; a < AU; ++a) {
-      const int h = h0 + a * RP + sub;
-      raw[a] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < h_end) {
-        const __nv_bfloat16* x;
-        if (h < p.Hq) x = p.q + b * p.st[0] + i * p.st[1] + h * p.st[2];
-        else if (h < p.Hq + p.Hkv) x = p.k + b * p.st[3] + i * p.st[4] + (h - p.Hq) * p.st[5];
-        else x = p.v + b * p.st[6] + i * p.st[7] + (h - p.Hq - p.Hkv) * p.st[8];
-        raw[a] = *reinterpret_cast<const uint4*>(x + 8 * u);
+      for (int a = 0; a < AU; ++a) {
+        const int at = h + a * RP + sub;
+        next[a] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < h1) next[a] = __ldcs(reinterpret_cast<const uint4*>(src + at * step));
+      }
+    };
+    load(h0);
+#pragma unroll 1
+    for (int h = h0; h < h1; h += RP * AU) {
+      uint4 raw[AU];
+#pragma unroll
+      for (int a = 0; a < AU; ++a) raw[a] = next[a];
+      if (h + RP * AU < h1) load(h + RP * AU);
+#pragma unroll
+      for (int a = 0; a < AU; ++a) {
+        if (h + a * RP >= h1) break;  // warp-uniform
+        const int at = h + a * RP + sub;
+        if (!plain) {
+          float x[8];
+          uint32_t* r = &raw[a].x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(r[e] << 16);
+            x[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+          }
+          if (w != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float g = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= g * wt[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y0, y1;
+            if (PAIRS) {
+              y0 = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
+              y1 = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
+            } else {
+              y0 = fmaf(x[2 * e], cs[2 * e % NA], __shfl_sync(0xffffffffu, x[2 * e], from) * sn[2 * e % NA]);
+              y1 = fmaf(x[2 * e + 1], cs[(2 * e + 1) % NA],
+                        __shfl_sync(0xffffffffu, x[2 * e + 1], from) * sn[(2 * e + 1) % NA]);
+            }
+            const __nv_bfloat162 t = turns ? __floats2bfloat162_rn(y0, y1) : __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            r[e] = *reinterpret_cast<const uint32_t*>(&t);
+          }
+        }
+        if (at < h1) *reinterpret_cast<uint4*>(dst + at * D) = raw[a];
       }
     }
-#pragma unroll
-    for (int a = 0; a < AU; ++a) {
-      if (h0 + a * RP >= h_end) break;  // warp-uniform
-      const int h = h0 + a * RP + sub;
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-      float x[8];
-      const uint32_t r[4] = {raw[a].x, raw[a].y, raw[a].z, raw[a].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(r[e] << 16);
-        x[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
-      }
-      if (p.wq != nullptr || p.wk != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const bool norm = is_q ? p.wq != nullptr : p.wk != nullptr;
-        const float g = norm ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= g * (is_q ? wq[e] : wk[e]);
-      }
-      float y[8];
-      if (PAIRS) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = x[2 * e] * cs[e % NA] - x[2 * e + 1] * sn[e % NA];
-          y[2 * e + 1] = x[2 * e + 1] * cs[e % NA] + x[2 * e] * sn[e % NA];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(0xffffffffu, x[e], src);
-          y[e] = turns ? fmaf(x[e], cs[e % NA], o * sn[e % NA]) : x[e];
-        }
-      }
-      if (PAIRS && !turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
-      }
-      uint4 w = raw[a];
-      if (!is_v) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 t = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&t);
-        }
-        w = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      if (h < h_end && (is_q || in_cache)) {
-        __nv_bfloat16* dst;
-        if (is_q) dst = p.q_out + (tok * p.Hq + h) * D;
-        else if (is_v) dst = p.v_cache + ((b * p.cap + row) * p.Hkv + (h - p.Hq - p.Hkv)) * D;
-        else dst = p.k_cache + ((b * p.cap + row) * p.Hkv + (h - p.Hq)) * D;
-        *reinterpret_cast<uint4*>(dst + 8 * u) = w;
-      }
-    }
-  }
+  };
+  const int lo = chunk * p.per, hi = min(p.Hq + 2 * p.Hkv, lo + p.per);
+  const int64_t cell = (b * p.cap + row) * p.Hkv * D + 8 * u;
+  rows(lo, min(hi, p.Hq), p.q + b * p.st[0] + i * p.st[1] + 8 * u, p.st[2], p.q_out + tok * p.Hq * D + 8 * u, p.wq, false);
+  if (!in_cache) return;
+  rows(max(lo - p.Hq, 0), min(hi - p.Hq, p.Hkv), p.k + b * p.st[3] + i * p.st[4] + 8 * u, p.st[5], p.k_cache + cell, p.wk,
+       false);
+  rows(max(lo - p.Hq - p.Hkv, 0), min(hi - p.Hq - p.Hkv, p.Hkv), p.v + b * p.st[6] + i * p.st[7] + 8 * u, p.st[8],
+       p.v_cache + cell, nullptr, true);
 }
 
 // ============================================================ evict
@@ -460,7 +455,9 @@ int ssa_cache_append(const void* q, const void* k, const void* v, const int64_t*
   int sms = 0;
   if (sm_count(&sms) != SSA_OK) return SSA_ERR_CUDA;
   // Few tokens: split a token's heads over warps until the GPU has about 16
-  // warps an SM to hide latency with; many tokens: one warp a token.
+  // warps an SM to hide latency with; many tokens: one warp a token, which computes
+  // the angles once.  (64 or 128 warps an SM: 55 and 61 us against 49 at 8,192
+  // tokens of 32 / 8 heads, since every warp computes them again.)
   const int rp = 32 / (d / 8), HT = Hq + 2 * Hkv;
   const int64_t tokens = (int64_t)B * L, most = (HT + rp - 1) / rp;
   int64_t chunks = ((int64_t)sms * 16 + tokens - 1) / tokens;

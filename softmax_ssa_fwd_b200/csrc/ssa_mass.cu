@@ -338,10 +338,11 @@ struct PromptSmem {
 // shared memory in rank order.  S = Q K^T, a thread a row and 64 of the keys:
 // its lse is one register and its 64 sums stay in registers over all row
 // tiles, added over the threads once at the end.  (A thread a key, as in the
-// stream kernel, reads a lse from shared memory for every exponential, which
-// goes through the same queue as they do: 340 us against 4 % below the figure
-// of this form at 8,192 rows and keys of 32 / 8 heads.)  256 keys, because every
-// row tile comes from L2, 32 KB (d = 128) in the 2,048 clocks of its exponentials.
+// stream kernel, reads a lse from shared memory for every exponential: 352 us
+// against 340 at 8,192 rows and keys of 32 / 8 heads, d = 128.)  256 keys, because
+// every row tile comes from L2, 32 KB in the 2,048 clocks of its exponentials.
+// Those take 79 % of all clocks; a quarter of them by a polynomial on the fp32
+// pipe changed nothing, so what is left lies between tiles and blocks.
 template <int D>
 __global__ void __launch_bounds__(NTP, 1)
     mass_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
