@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from typing import NamedTuple
 
@@ -190,6 +191,11 @@ def append(q, k, v, k_cache, v_cache, positions=None, *, inv_freq=None, axis=Non
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(dev, B, T, Hq, Hkv, cap, d):
+    return max(16, ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d))
+
+
 def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of T drafted tokens per sequence (q [B, T, Hq, d]) over its cache k, v [B, cap, Hkv, d]:
     the keys before lens[b], and draft key t (row lens[b] + t) where bit t of tree_mask[b, i] is set.
@@ -215,8 +221,7 @@ def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, wor
         if lse is None:
             lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = torch.empty(max(16, ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d)), dtype=torch.uint8,
-                                    device=dev)
+            workspace = torch.empty(_tree_workspace(dev, B, T, Hq, Hkv, cap, d), dtype=torch.uint8, device=dev)
         if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
             raise SSAError(SSA_ERR_INVALID_ARG, f"workspace: want a contiguous tensor on cuda:{dev}")
         op = _tensor(out, "out", torch.bfloat16, (B, T, Hq, d), dev)

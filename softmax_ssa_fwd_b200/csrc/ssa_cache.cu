@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(32 * AW) append_kernel(const __grid_constant__
 // index order, so ties go to the lower index whatever the blocks' order.
 constexpr int ST = 1024, SW = ST / 32;
 constexpr int BINS = 2048;
+constexpr int MU = 8;
 constexpr int MAX_KEYS = 40960;  // keys of a block's slice kept in shared memory (160 KB)
 
 struct EvictParams {
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(ST, 1) evict_select_kernel(const EvictParams p
   __shared__ uint32_t s_warp[SW], s_warp2[SW];
   __shared__ uint32_t s_digit, s_want;
   __shared__ uint32_t s_tot[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -244,10 +246,17 @@ __global__ void __launch_bounds__(ST, 1) evict_select_kernel(const EvictParams p
     hist[tid + ST] = 0u;
     __syncthreads();
     if (pass == 0 && cached) {
-      for (int j = tid; j < len; j += ST) {
-        const uint32_t x = mass_key(mine[j]);
-        s_keys[j] = x;
-        atomicAdd(&hist[x >> 21], 1u);
+      for (int j0 = tid; j0 < len; j0 += MU * ST) {  // MU loads on their way at once
+        float v[MU];
+#pragma unroll
+        for (int e = 0; e < MU; ++e) v[e] = j0 + e * ST < len ? mine[j0 + e * ST] : 0.f;
+#pragma unroll
+        for (int e = 0; e < MU; ++e) {
+          if (j0 + e * ST >= len) break;
+          const uint32_t x = mass_key(v[e]);
+          s_keys[j0 + e * ST] = x;
+          atomicAdd(&hist[x >> 21], 1u);
+        }
       }
     } else {
       for (int j = tid; j < len; j += ST) {
@@ -355,7 +364,8 @@ __global__ void __launch_bounds__(ST, 1) evict_select_kernel(const EvictParams p
   cluster.sync();  // the others may still read this block's totals
 }
 
-// Compaction: D / 8 lanes a row, key heads fastest (the output's order).
+// Compaction: D / 8 lanes a row, key heads fastest (the output's order).  Launched
+// early, it waits for the selection.
 constexpr int GT = 256, GU = 2;
 
 template <int D>
@@ -365,6 +375,7 @@ __global__ void __launch_bounds__(GT) evict_gather_kernel(const EvictParams p) {
   const int64_t total = (int64_t)p.B * p.keep * p.Hkv;
   uint4 kv[2 * GU];
   int64_t dst[GU];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
   for (int a = 0; a < GU; ++a) {
     const int64_t r = ((int64_t)blockIdx.x * GU + a) * ROWS + g;
@@ -547,9 +558,15 @@ int ssa_cache_evict(const void* k, const void* v, const float* mass, const int32
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return SSA_ERR_CUDA;
-  if (d == 128) evict_gather_kernel<128><<<(unsigned)grid, GT, 0, st>>>(p);
-  else evict_gather_kernel<64><<<(unsigned)grid, GT, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SSA_OK : SSA_ERR_CUDA;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(GT);
+  cfg.dynamicSmemBytes = 0;
+  return (d == 128 ? cudaLaunchKernelEx(&cfg, evict_gather_kernel<128>, p)
+                   : cudaLaunchKernelEx(&cfg, evict_gather_kernel<64>, p)) == cudaSuccess
+             ? SSA_OK
+             : SSA_ERR_CUDA;
 }
 
 }  // extern "C"
