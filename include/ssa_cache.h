@@ -23,6 +23,8 @@
  *     ssa_decode_tree or ssa_attn_mass on a device allocates the 4-byte status
  *     word that ssa_device_status reads: make it (or any ssa_fwd / ssa_decode
  *     call) before capturing a graph.
+ *   - An output must not lie over an input, over the workspace or over another
+ *     output (SSA_ERR_INVALID_ARG), but for the two cases named below.
  *   - Results do not depend on the order in which blocks run: the same call
  *     on the same GPU gives the same bits.
  */
@@ -110,7 +112,7 @@ size_t ssa_decode_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int cap, i
  *   lens: int32 [B], NULL for cap
  *   mass_in, mass_out: fp32 [B, Hkv, cap]; mass_in NULL counts as 0 (decay is
  *   then not used); mass_out may be mass_in.  decay finite, >= 0.
- *   Limit: B <= 1024 (SSA_ERR_UNSUPPORTED otherwise). */
+ *   Limits: B <= 1024, Hq / Hkv <= 128 (SSA_ERR_UNSUPPORTED otherwise). */
 int ssa_attn_mass(const void* q, const void* k, const float* lse, const int32_t* lens,
                   const float* mass_in, float* mass_out, int B, int Lq, int window, int Hq, int Hkv,
                   int cap, int d, int causal, float scale, float decay, void* stream);
@@ -122,11 +124,10 @@ int ssa_attn_mass(const void* q, const void* k, const float* lse, const int32_t*
  * ascending order.
  *   k, v:         bf16 [B, cap, Hkv, d];  mass: fp32 [B, Hkv, cap]
  *   k_out, v_out: bf16 [B, cap_out, Hkv, d], cap_out >= keep; rows past the kept
- *                 ones keep what they hold.  No overlap with k, v.
+ *                 ones keep what they hold.
  *   mass_out:     fp32 [B, Hkv, cap_out]: the kept masses, 0 past them.
  *   index_out:    int32 [B, Hkv, keep]: the kept rows of k, -1 past them.
  *   lens_out:     int32 [B]: min(lens[b], keep).
- *   The outputs must not overlap the inputs or one another (SSA_ERR_INVALID_ARG).
  *   keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep. */
 int ssa_cache_evict(const void* k, const void* v, const float* mass, const int32_t* lens,
                     void* k_out, void* v_out, float* mass_out, int32_t* index_out,

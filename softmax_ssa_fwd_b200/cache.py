@@ -192,8 +192,18 @@ def append(q, k, v, k_cache, v_cache, positions=None, *, inv_freq=None, axis=Non
 
 
 @functools.lru_cache(maxsize=256)
-def _tree_workspace(dev, B, T, Hq, Hkv, cap, d):
-    return max(16, ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d))
+def _known_workspace(dev, B, T, Hq, Hkv, cap, d):
+    n = ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d)
+    if n == 0:
+        raise LookupError  # (not kept)
+    return n
+
+
+def _tree_workspace(*shape):
+    try:
+        return _known_workspace(*shape)
+    except LookupError:
+        return 16  # a shape that the call itself refuses
 
 
 def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, workspace=None, stream=None):

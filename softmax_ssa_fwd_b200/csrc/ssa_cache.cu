@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(32 * AW) append_kernel(const __grid_constant__
     if (h0 >= h1) return;
     float wt[8];
     if (w != nullptr) {
-      const float4 a = reinterpret_cast<const float4*>(w + 8 * u)[0], c = reinterpret_cast<const float4*>(w + 8 * u)[1];
-      wt[0] = a.x, wt[1] = a.y, wt[2] = a.z, wt[3] = a.w, wt[4] = c.x, wt[5] = c.y, wt[6] = c.z, wt[7] = c.w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wt[e] = w[8 * u + e];  // (4-byte aligned)
     }
     uint4 next[AU];
     auto load = [&](int h) {
@@ -434,6 +434,19 @@ int ssa_cache_append(const void* q, const void* k, const void* v, const int64_t*
     if (strides[i] < 0 || strides[i] % 8 != 0) return SSA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return SSA_ERR_UNSUPPORTED;
   if (rot % 16 != 0 || rot > d || axes < 1 || axes > 4) return SSA_ERR_UNSUPPORTED;
+  const size_t cache_bytes = (size_t)B * cap * Hkv * d * 2, out_bytes = (size_t)B * L * Hq * d * 2;
+  auto extent = [&](const int64_t* st, int heads) {
+    return (size_t)((B - 1) * st[0] + (L - 1) * st[1] + (heads - 1) * st[2] + d) * 2;
+  };
+  const ssa::Span in[3] = {{q, extent(strides, Hq)}, {k, extent(strides + 3, Hkv)}, {v, extent(strides + 6, Hkv)}};
+  const ssa::Span made[3] = {{k_cache, cache_bytes}, {v_cache, cache_bytes}, {q_out, out_bytes}};
+  const bool in_place = q_out == q && (Hq == 1 || strides[2] == d) && (L == 1 || strides[1] == (int64_t)Hq * d) &&
+                        (B == 1 || strides[0] == (int64_t)L * Hq * d);
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (ssa::overlap(made[i], in[j]) && !(i == 2 && j == 0 && in_place)) return SSA_ERR_INVALID_ARG;
+    if (ssa::overlap(made[i], made[(i + 1) % 3])) return SSA_ERR_INVALID_ARG;
+  }
   AppendParams p{};
   for (int i = 0; i < rot / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return SSA_ERR_INVALID_ARG;
@@ -507,15 +520,13 @@ int ssa_cache_evict(const void* k, const void* v, const float* mass, const int32
   const int64_t rows = (int64_t)pairs * keep, per = (int64_t)GT / (d / 8) * GU;
   const int64_t grid = (rows + per - 1) / per;
   if (pairs > (1u << 24) || grid > 0x7fffffff || cap > (1 << 30)) return SSA_ERR_UNSUPPORTED;
-  const struct { const void* at; size_t bytes; } span[9] = {
+  const ssa::Span span[9] = {
       {k_out, pairs * cap_out * d * 2}, {v_out, pairs * cap_out * d * 2}, {mass_out, pairs * cap_out * 4},
       {index_out, pairs * keep * 4},    {lens_out, (size_t)B * 4},        {k, pairs * cap * d * 2},
       {v, pairs * cap * d * 2},         {mass, pairs * cap * 4},          {lens, (size_t)B * 4}};
   for (int i = 0; i < 5; ++i)  // each output against every other tensor
-    for (int j = i + 1; j < 9; ++j) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(span[i].at), y = reinterpret_cast<uintptr_t>(span[j].at);
-      if (x < y + span[j].bytes && y < x + span[i].bytes) return SSA_ERR_INVALID_ARG;
-    }
+    for (int j = i + 1; j < 9; ++j)
+      if (ssa::overlap(span[i], span[j])) return SSA_ERR_INVALID_ARG;
   EvictParams p{};
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);

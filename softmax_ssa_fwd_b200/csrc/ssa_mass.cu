@@ -77,7 +77,8 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, float* x) {
   else ssa::tmem_ld32f(taddr, x);
 }
 
-// Adds exp2(s c + nl) over NC columns; columns below `first` do not count.
+// Adds exp2(s c + nl) over NC columns.  MASK: columns below `first`, and those without
+// a lse, whose scores may be anything, do not count.
 template <int NC, bool MASK>
 __device__ __forceinline__ void add_columns(const float* x, const float* nl, float c, int first, uint64_t (&acc)[2]) {
   const uint64_t c2 = ssa::f2_pack(c, c);
@@ -92,8 +93,8 @@ __device__ __forceinline__ void add_columns(const float* x, const float* nl, flo
       ssa::f2_unpack(e, e0, e1);
       float p0 = ex2(e0), p1 = ex2(e1);
       if (MASK) {
-        p0 = i + 2 * h >= first ? p0 : 0.f;
-        p1 = i + 2 * h + 1 >= first ? p1 : 0.f;
+        p0 = i + 2 * h >= first && (h ? l.z : l.x) > -INFINITY ? p0 : 0.f;
+        p1 = i + 2 * h + 1 >= first && (h ? l.w : l.y) > -INFINITY ? p1 : 0.f;
       }
       acc[h] = ssa::fadd2(acc[h], ssa::f2_pack(p0, p1));
     }
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(NT, 1)
   __shared__ uint64_t half_full[2], half_empty[2];
   __shared__ float half_sum[2][BK];
   __shared__ __align__(16) float nlse[2][N];
+  __shared__ int bare[2];  // some column has no lse
   __shared__ int pref[ssa::MAX_SEQS + 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -256,8 +258,15 @@ __global__ void __launch_bounds__(NT, 1)
         for (int c = 0; c < D / 64; ++c)
           ssa::tma_load_4d(q_s + c * N * 128, &tm_q, smem_u32(&q_full), c * 64, s.in * p.G, p.Lq - p.W, s.b);
       }
-      for (int r = lane; r < N; r += 32)
-        nlse[n & 1][r] = r < p.G * p.W ? neg_lse2(p, s.b, s.in, r) : -INFINITY;
+      bool none = false;
+#pragma unroll 1
+      for (int r = lane; r < N; r += 32) {
+        const float l = r < p.G * p.W ? neg_lse2(p, s.b, s.in, r) : -INFINITY;
+        none |= l == -INFINITY;
+        nlse[n & 1][r] = l;
+      }
+      none = __any_sync(0xffffffffu, none);
+      if (lane == 0) bare[n & 1] = none;
       mbar_arrive(smem_u32(&lse_full[n & 1]));
       ++n;
     }
@@ -287,9 +296,10 @@ __global__ void __launch_bounds__(NT, 1)
         if (!ok) break;
         ssa::tc_fence_after();
         // row i of the window sits at i + len - W: key j counts from there on
-        const bool mask = p.causal && j0 + BK - 1 > len - p.W;
+        const bool mask = bare[n & 1] || (p.causal && j0 + BK - 1 > len - p.W);
+        const int first = p.causal ? (j - len + p.W) * p.G - NC * half : 0;
         uint64_t acc[2] = {ssa::f2_pack(0.f, 0.f), ssa::f2_pack(0.f, 0.f)};
-        add_tile<NC>(lanes, &nlse[n & 1][NC * half], p.c, mask, (j - len + p.W) * p.G - NC * half, acc, [&] {
+        add_tile<NC>(lanes, &nlse[n & 1][NC * half], p.c, mask, first, acc, [&] {
           ssa::tc_fence_before();  // S is in registers: the buffer is free
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
@@ -591,6 +601,12 @@ extern "C" int ssa_attn_mass(const void* q, const void* k, const float* lse, con
   if (d != 64 && d != 128) return SSA_ERR_UNSUPPORTED;
   if (B > ssa::MAX_SEQS || Hq / Hkv > BN) return SSA_ERR_UNSUPPORTED;
   if ((long long)B * Hkv > (1 << 24) || (long long)Lq * Hq > 0x7fffffff || cap > (1 << 30)) return SSA_ERR_UNSUPPORTED;
+  const size_t mass_bytes = (size_t)B * Hkv * cap * 4;
+  const ssa::Span made{mass_out, mass_bytes};
+  const ssa::Span in[5] = {{q, (size_t)B * Lq * Hq * d * 2}, {k, (size_t)B * cap * Hkv * d * 2}, {lse, (size_t)B * Hq * Lq * 4},
+                           {lens, (size_t)B * 4}, {mass_in == mass_out ? nullptr : mass_in, mass_bytes}};
+  for (const ssa::Span& x : in)
+    if (ssa::overlap(made, x)) return SSA_ERR_INVALID_ARG;
   Params p{};
   p.lse = lse;
   p.mass_in = mass_in;

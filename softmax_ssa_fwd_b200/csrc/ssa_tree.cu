@@ -1188,6 +1188,12 @@ int ssa_decode_tree(const void* q, const void* k, const void* v, void* out, floa
        reinterpret_cast<uintptr_t>(tree_mask)) & 3u)
     return SSA_ERR_INVALID_ARG;
   if (!supported(B, T, Hq, Hkv, cap, d)) return SSA_ERR_UNSUPPORTED;
+  const size_t rows = (size_t)B * T * Hq, cache = (size_t)B * cap * Hkv * d * 2;
+  const ssa::Span span[8] = {{out, rows * d * 2}, {lse, rows * 4}, {workspace, workspace_bytes}, {q, rows * d * 2},
+                             {k, cache}, {v, cache}, {lens, (size_t)B * 4}, {tree_mask, (size_t)B * T * ((T + 31) / 32) * 4}};
+  for (int i = 0; i < 3; ++i)  // each output against every other tensor
+    for (int j = i + 1; j < 8; ++j)
+      if (ssa::overlap(span[i], span[j])) return SSA_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != SSA_OK) return SSA_ERR_CUDA;
   const Plan x = plan(B, T, Hq, Hkv, cap, sms);

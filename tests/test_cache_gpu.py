@@ -122,6 +122,16 @@ def test_append(cache, B, L, Hq, Hkv, d, rot, pairs, axes, norm):
         assert torch.equal(again[b, :n], got[b, :n]) and torch.equal(kc2[b, s:s + n], kc[b, s:s + n])
 
 
+def test_append_weights_need_four_byte_alignment_only(cache):
+    B, L, Hq, Hkv, d = 1, 3, 2, 1, 64
+    q, k, v = _rand(1, B, L, Hq, d).cuda(), _rand(2, B, L, Hkv, d).cuda(), _rand(3, B, L, Hkv, d).cuda()
+    w = torch.randn(2 * d + 3, generator=torch.Generator().manual_seed(1)).cuda()
+    kc = torch.zeros(2, B, L, Hkv, d, dtype=BF, device="cuda")
+    one = cache.append(q, k, v, kc[0], kc[1], q_weight=w[1:1 + d], k_weight=w[d + 3:])
+    also = cache.append(q, k, v, kc[1].clone(), kc[1], q_weight=w[1:1 + d].clone(), k_weight=w[d + 3:].clone())
+    assert torch.equal(one, also)
+
+
 def test_append_far_positions_and_rows_outside_the_cache(cache):
     # the same angle at far positions: 2^30 turns of a frequency that divides the circle differ from none
     L, d = 5, 64
@@ -284,6 +294,7 @@ MASS = [
     (1, 3, 128, 1, 64, [200], 200, True, 0, None),         # G = 128
     (2, 20, 4, 4, 64, [0, 30], 300, True, 0, 1.0),         # nothing cached
     (1, 20, 2, 2, 64, [12], 40, True, 0, None),            # rows before the first key: left-padded
+    (1, 300, 4, 2, 64, [100], 150, True, 0, None),         # the same with many rows
     (30, 3, 2, 1, 64, [(37 * b) % 500 for b in range(30)], 500, True, 0, 0.5),
 ]
 
@@ -326,6 +337,28 @@ def test_attn_mass(cache, B, Lq, Hq, Hkv, d, lens, cap, causal, window, decay):
     elif window == 0 and causal and int(lens.min()) >= Lq:  # every row's weights sum to 1
         total = got.sum((1, 2)).cpu()
         assert (total - Hq * Lq).abs().max() <= 1e-3 * Hq * Lq
+
+
+@pytest.mark.parametrize("junk", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Lq", [3, 64, 200])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attn_mass_rows_without_keys_may_hold_anything(cache, causal, Lq, junk):
+    B, Hq, Hkv, d, n = 1, 4, 1, 64, 333
+    q, k, lens = _rand(1, B, Lq, Hq, d), _rand(2, B, n, Hkv, d), _i32([n])
+    lse = _lse(q, k, lens, causal, 0.125)
+    lse[:, 1, Lq // 2] = lse[:, :, 0] = -np.inf
+    want, dots, args = oracle.attn_mass(q, k, lse, lens, causal, 0.125, 0, None, 1.0)
+    q[:, Lq // 2, 1] = q[:, 0] = junk
+    got = cache.attn_mass(q.cuda(), k.cuda(), lse.cuda(), lens=lens.cuda(), causal=causal)
+    _near(got, want, d * 2.0 ** -23 * dots + 2.0 ** -22 * args + 2.0 ** -14 * want, "mass")
+
+
+def test_attn_mass_of_an_infinite_key(cache):
+    """Its score with the one row is -inf: no weight (rows that are not there must not make it NaN)."""
+    q, k = torch.full((1, 1, 1, 64), -1.0).to(BF).cuda(), _rand(2, 1, 200, 1, 64).cuda()
+    k[0, 7, 0, 3] = float("inf")
+    got = cache.attn_mass(q, k, torch.zeros(1, 1, 1, device="cuda"), causal=False)
+    assert got[0, 0, 7] == 0 and torch.isfinite(got).all()
 
 
 # ------------------------------------------------------------------ evict

@@ -68,6 +68,20 @@ def test_append_invalid_host_arrays(cache):
     assert _append(cache, axes=2, axis=[-1] + [0] * 63) == -1
 
 
+@pytest.mark.parametrize("over", [
+    dict(kc=0x10000), dict(vc=0x20000 + 0x400), dict(vc=0x80000), dict(kc=0x70000), dict(out=0x20000), dict(out=0x30000),
+    dict(out=0x10000 + 0x100), dict(out=0x10000, strides=[1664, 544, 136, 768, 256, 128, 768, 256, 128]),
+])
+def test_append_outputs_over_other_tensors(cache, over):
+    assert _append(cache, **over) == -1
+
+
+def test_append_over_its_own_queries_is_allowed(cache):
+    if torch.cuda.is_available():
+        pytest.skip("needs the no-GPU path")
+    assert _append(cache) == _append(cache, out=0x10000) == -3  # on to CUDA, which is not there
+
+
 @pytest.mark.parametrize("over", [dict(d=96, rot=0), dict(rot=24), dict(rot=144), dict(axes=0), dict(axes=5),
                                   dict(d=64)])
 def test_append_unsupported(cache, over):
@@ -75,8 +89,8 @@ def test_append_unsupported(cache, over):
 
 
 def _tree(cache, **over):
-    a = dict(q=0x10000, k=0x20000, v=0x30000, out=0x40000, lse=0x50000, lens=0x60000, mask=0x70000, B=2, T=4, Hq=8,
-             Hkv=2, cap=300, d=128, scale=0.1, ws=0x80000, wsb=1 << 40)
+    a = dict(q=0x10000000, k=0x20000000, v=0x30000000, out=0x40000000, lse=0x50000000, lens=0x60000000, mask=0x70000000,
+             B=2, T=4, Hq=8, Hkv=2, cap=300, d=128, scale=0.1, ws=0x80000000, wsb=1 << 30)
     a.update(over)
     return cache.ssa_decode_tree(*a.values(), None)
 
@@ -84,8 +98,10 @@ def _tree(cache, **over):
 @pytest.mark.parametrize("over", [
     dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(lse=0), dict(lens=0), dict(mask=0), dict(ws=0), dict(B=0),
     dict(T=0), dict(Hq=0), dict(Hkv=0), dict(cap=0), dict(d=-64), dict(Hq=7), dict(scale=0.0), dict(scale=-1.0),
-    dict(scale=math.nan), dict(scale=math.inf), dict(q=0x10008), dict(v=0x30002), dict(ws=0x80004), dict(lse=0x50002),
-    dict(lens=0x60001), dict(mask=0x70002),
+    dict(scale=math.nan), dict(scale=math.inf), dict(q=0x10000008), dict(v=0x30000002), dict(ws=0x80000004), dict(lse=0x50000002),
+    dict(lens=0x60000001), dict(mask=0x70000002),
+    dict(out=0x10000000), dict(out=0x20000000), dict(lse=0x10000040), dict(ws=0x30000000), dict(lse=0x60000000),
+    dict(out=0x50000000 - 0x1000), dict(ws=0x40000000, wsb=1 << 30),
 ])
 def test_tree_invalid(cache, over):
     assert _tree(cache, **over) == -1
@@ -100,7 +116,7 @@ def test_tree_unsupported(cache, over):
 
 
 def _mass(cache, **over):
-    a = dict(q=0x10000, k=0x20000, lse=0x30000, lens=0x40000, min=0x50000, out=0x60000, B=2, Lq=4, window=0, Hq=8, Hkv=2,
+    a = dict(q=0x10000000, k=0x20000000, lse=0x30000000, lens=0x40000000, min=0x50000000, out=0x60000000, B=2, Lq=4, window=0, Hq=8, Hkv=2,
              cap=300, d=128, causal=1, scale=0.1, decay=0.5)
     a.update(over)
     return cache.ssa_attn_mass(*a.values(), None)
@@ -109,8 +125,9 @@ def _mass(cache, **over):
 @pytest.mark.parametrize("over", [
     dict(q=0), dict(k=0), dict(lse=0), dict(out=0), dict(B=0), dict(Lq=0), dict(window=-1), dict(window=5), dict(Hq=0),
     dict(Hkv=0), dict(Hq=9), dict(cap=0), dict(d=0), dict(scale=0.0), dict(scale=math.inf), dict(decay=-0.1),
-    dict(decay=math.nan), dict(decay=math.inf), dict(q=0x10004), dict(k=0x20008), dict(lse=0x30002), dict(min=0x50001),
-    dict(out=0x60002), dict(lens=0x40002),
+    dict(decay=math.nan), dict(decay=math.inf), dict(q=0x10000004), dict(k=0x20000008), dict(lse=0x30000002),
+    dict(min=0x50000001), dict(out=0x60000002), dict(lens=0x40000002), dict(out=0x10000000), dict(out=0x20000000),
+    dict(out=0x30000000), dict(out=0x40000000), dict(out=0x50000004),
 ])
 def test_mass_invalid(cache, over):
     assert _mass(cache, **over) == -1
