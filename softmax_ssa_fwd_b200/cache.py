@@ -83,27 +83,35 @@ def _heads(x, name):
 def _strided(x, name, shape, dev):
     """The batch, token and head stride of a tensor whose heads' columns are contiguous."""
     s = x.stride() if isinstance(x, torch.Tensor) else ()
-    if not (x.dtype is torch.bfloat16 and x.shape == shape and x.get_device() == dev and s[3] == 1):
+    if not (s and x.dtype is torch.bfloat16 and x.shape == shape and x.get_device() == dev and s[3] == 1):
         _refuse(name + " (columns of a head contiguous)", torch.bfloat16, shape, dev, contiguous=False)
     return s[:3]
+
+
+# (as torch's own generated code asks; the public calls build objects and cost as much as a launch)
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _On:
     """Makes the device of a call current, and a stream that the caller named; torch's allocations inside follow it."""
 
+    __slots__ = ("dev", "stack")
+
     def __init__(self, dev, stream):
         self.dev, self.stack = dev, None
-        if stream is not None or torch.cuda.current_device() != dev:
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            _need(stream.device.index == dev, "stream: belongs to another device than the tensors")
+        if stream is not None or _device() != dev:
             self.stack = contextlib.ExitStack()
             self.stack.enter_context(torch.cuda.device(dev))
             if stream is not None:
-                if not isinstance(stream, torch.cuda.Stream):
-                    stream = torch.cuda.ExternalStream(int(stream), device=dev)
-                _need(stream.device.index == dev, "stream: belongs to another device than the tensors")
                 self.stack.enter_context(torch.cuda.stream(stream))
 
     def __enter__(self):
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.dev)
 
     def __exit__(self, *e):
         if self.stack is not None:
@@ -184,7 +192,9 @@ def append(q, k, v, k_cache, v_cache, positions=None, *, inv_freq=None, axis=Non
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(B, L, Hq, d, dtype=torch.bfloat16, device=dev)
-        qo = _tensor(out, "out", torch.bfloat16, (B, L, Hq, d), dev)
+            qo = out.data_ptr()
+        else:
+            qo = _tensor(out, "out", torch.bfloat16, q.shape, dev)
         _done(ssa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, wq, wk, eps, pos, freq, ax, axes, rot,
                                int(interleaved), factor, s0, cnt, qo, kc, vc, B, L, Hq, Hkv, d, cap, st),
               "ssa_cache_append")
@@ -227,15 +237,19 @@ def decode_tree(q, k, v, lens, tree_mask, *, scale=None, out=None, lse=None, wor
         scale = d ** -0.5
     with _On(dev, stream) as st:
         if out is None:
-            out = torch.empty(B, T, Hq, d, dtype=torch.bfloat16, device=dev)
+            out = torch.empty_like(q)
+            op = out.data_ptr()
+        else:
+            op = _tensor(out, "out", torch.bfloat16, q.shape, dev)
         if lse is None:
             lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+            sp = lse.data_ptr()
+        else:
+            sp = _tensor(lse, "lse", torch.float32, (B, Hq, T), dev)
         if workspace is None:
             workspace = torch.empty(_tree_workspace(dev, B, T, Hq, Hkv, cap, d), dtype=torch.uint8, device=dev)
-        if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
+        elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous()):
             raise SSAError(SSA_ERR_INVALID_ARG, f"workspace: want a contiguous tensor on cuda:{dev}")
-        op = _tensor(out, "out", torch.bfloat16, (B, T, Hq, d), dev)
-        sp = _tensor(lse, "lse", torch.float32, (B, Hq, T), dev)
         _done(ssa_decode_tree(qp, kp, vp, op, sp, lp, mp, B, T, Hq, Hkv, cap, d, scale, workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), st), "ssa_decode_tree")
     return out, lse
@@ -254,12 +268,15 @@ def attn_mass(q, k, lse, *, lens=None, causal=True, scale=None, window=0, mass=N
     sp = _tensor(lse, "lse", torch.float32, (B, Hq, Lq), dev)
     lp = _optional(lens, "lens", torch.int32, (B,), dev)
     mp = _optional(mass, "mass", torch.float32, (B, Hkv, cap), dev)
+    _need(0 <= window <= Lq, "window: want 0 (all rows) to Lq")
     if scale is None:
         scale = d ** -0.5
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(B, Hkv, cap, dtype=torch.float32, device=dev)
-        op = _tensor(out, "out", torch.float32, (B, Hkv, cap), dev)
+            op = out.data_ptr()
+        else:
+            op = _tensor(out, "out", torch.float32, (B, Hkv, cap), dev)
         _done(ssa_attn_mass(qp, kp, sp, lp, mp, op, B, Lq, window, Hq, Hkv, cap, d, int(causal), scale, decay, st),
               "ssa_attn_mass")
     return out
@@ -286,27 +303,24 @@ def evict(k, v, mass, lens, *, keep, sink=0, recent=0, k_out=None, v_out=None, m
     vp = _tensor(v, "v", torch.bfloat16, k.shape, dev)
     mp = _tensor(mass, "mass", torch.float32, (B, Hkv, cap), dev)
     lp = _tensor(lens, "lens", torch.int32, (B,), dev)
-    _need(keep >= 1 and sink >= 0 and recent >= 0 and sink + recent <= keep, "keep, sink, recent: want sink + recent <= keep")
+    _need(1 <= keep < 2 ** 31 and sink >= 0 and recent >= 0 and sink + recent <= keep, "keep, sink, recent: want sink + recent <= keep")
     with _On(dev, stream) as st:
         cap_out = keep
         for t, name in ((k_out, "k_out"), (v_out, "v_out")):
             if t is not None:
                 cap_out = _heads(t, name)[1]
-        if k_out is None:
-            k_out = torch.empty(B, cap_out, Hkv, d, dtype=torch.bfloat16, device=dev)
-        if v_out is None:
-            v_out = torch.empty(B, cap_out, Hkv, d, dtype=torch.bfloat16, device=dev)
-        if mass_out is None:
-            mass_out = torch.empty(B, Hkv, cap_out, dtype=torch.float32, device=dev)
-        if index is None:
-            index = torch.empty(B, Hkv, keep, dtype=torch.int32, device=dev)
-        if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        ko = _tensor(k_out, "k_out", torch.bfloat16, (B, cap_out, Hkv, d), dev)
-        vo = _tensor(v_out, "v_out", torch.bfloat16, (B, cap_out, Hkv, d), dev)
-        mo = _tensor(mass_out, "mass_out", torch.float32, (B, Hkv, cap_out), dev)
-        io = _tensor(index, "index", torch.int32, (B, Hkv, keep), dev)
-        lo = _tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+
+        def output(t, name, dtype, *shape):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=dev)
+                return t, t.data_ptr()
+            return t, _tensor(t, name, dtype, shape, dev)
+
+        k_out, ko = output(k_out, "k_out", torch.bfloat16, B, cap_out, Hkv, d)
+        v_out, vo = output(v_out, "v_out", torch.bfloat16, B, cap_out, Hkv, d)
+        mass_out, mo = output(mass_out, "mass_out", torch.float32, B, Hkv, cap_out)
+        index, io = output(index, "index", torch.int32, B, Hkv, keep)
+        new_lens, lo = output(new_lens, "new_lens", torch.int32, B)
         _done(ssa_cache_evict(kp, vp, mp, lp, ko, vo, mo, io, lo, B, Hkv, cap, cap_out, d, keep, sink, recent, st),
               "ssa_cache_evict")
     return Evicted(k_out, v_out, mass_out, index, new_lens)
