@@ -456,6 +456,41 @@ def test_a_generation(cache):
     assert more.shape == small.mass.shape and torch.isfinite(more).all()
 
 
+def test_offsets_past_32_bits(cache):
+    """The second sequence of a cache of 2.9e9 elements gives what it gives on its own."""
+    B, T, Hq, Hkv, d, cap = 2, 2, 32, 16, 128, 700000
+    k, v = torch.zeros(B, cap, Hkv, d, dtype=BF, device="cuda"), torch.zeros(B, cap, Hkv, d, dtype=BF, device="cuda")
+    x = _rand(1, B, T, Hq + 2 * Hkv, d).cuda()
+    qkv = x.split([Hq, Hkv, Hkv], 2)
+    k[1, -300:] = 2 * _rand(2, 300, Hkv, d).cuda()
+    v[1, -300:] = _rand(3, 300, Hkv, d).cuda()
+    lens = _i32([5, cap - T]).cuda()
+    q = cache.append(*qkv, k, v, start=lens)
+    assert torch.equal(k[1, -T:], qkv[1][1]) and torch.equal(v[1, -T:], qkv[2][1]) and torch.equal(k[0, 5:7], qkv[1][0])
+    mask = _mask("chain", B, T, 0).cuda()
+    o, lse = cache.decode_tree(q, k, v, lens, mask)
+    o1, lse1 = cache.decode_tree(q[1:], k[1:], v[1:], lens[1:], mask[1:])
+    # the same sums cut elsewhere: two roundings of the weights and the result, values below 5
+    assert (o[1:].float() - o1.float()).abs().max() <= 4 * H * 5 and (lse[1:] - lse1).abs().max() <= 2.0 ** -14
+    m = cache.attn_mass(q, k, lse, lens=lens + T)
+    m1 = cache.attn_mass(q[1:], k[1:], lse[1:], lens=lens[1:] + T)
+    assert torch.equal(m[1:], m1) and (m.sum((1, 2)) - Hq * T).abs().max() <= 0.01 * Hq * T
+    small, one = (cache.evict(a, b, c, n, keep=64, sink=1, recent=2) for a, b, c, n in
+                  ((k, v, m, lens + T), (k[1:], v[1:], m1, lens[1:] + T)))
+    assert torch.equal(small.index[1:], one.index) and torch.equal(small.k[1:], one.k) and torch.equal(small.v[1:], one.v)
+    assert one.index[0, :, -1].tolist() == [cap - 1] * Hkv
+    assert torch.equal(one.k[0, -1], k[1, -1]) and torch.equal(one.v[0, -1], v[1, -1])
+
+
+def test_as_many_sequences_as_allowed(cache):
+    B, T, Hq, Hkv, d, cap = 1024, 1, 2, 1, 64, 260
+    q, k, v = _rand(1, B, T, Hq, d), _rand(2, B, cap, Hkv, d), _rand(3, B, cap, Hkv, d)
+    lens = _i32([(37 * b) % 260 for b in range(B)])
+    o, lse = _tree_check(cache, q, k, v, lens, _mask("chain", B, T, 0))
+    got = cache.attn_mass(q.cuda(), k.cuda(), lse, lens=lens.cuda() + 1).sum((1, 2))
+    assert (got - Hq).abs().max() <= 1e-3
+
+
 def test_replay_reads_the_lengths_of_the_moment(cache):
     B, T, Hq, Hkv, d, cap = 2, 3, 8, 2, 128, 900
     q, k, v = _rand(1, B, T, Hq, d).cuda(), _rand(2, B, cap, Hkv, d).cuda(), _rand(3, B, cap, Hkv, d).cuda()
