@@ -62,13 +62,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// -lse in log2 units; a row without keys (-inf) and a row that is not there get
-// -inf, so that their exponentials are 0
+// -lse in log2 units; +inf, which only a lse of -inf gives, marks a row that has
+// no keys or is not there: its exponentials do not count.  (NaN and +inf do.)
 __device__ __forceinline__ float neg_lse2(const Params& p, int b, int hkv, int r) {
   const int i = p.Lq - p.W + r / p.G;
-  if (i >= p.Lq) return -INFINITY;
-  const float l = p.lse[((size_t)b * p.Hq + hkv * p.G + r % p.G) * p.Lq + i];
-  return l == -INFINITY ? -INFINITY : -l * LOG2E;
+  if (i >= p.Lq) return INFINITY;
+  return -p.lse[((size_t)b * p.Hq + hkv * p.G + r % p.G) * p.Lq + i] * LOG2E;
 }
 
 template <int NC>
@@ -77,8 +76,8 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, float* x) {
   else ssa::tmem_ld32f(taddr, x);
 }
 
-// Adds exp2(s c + nl) over NC columns.  MASK: columns below `first`, and those without
-// a lse, whose scores may be anything, do not count.
+// Adds exp2(s c + nl) over NC columns.  MASK: columns below `first`, and rows without
+// keys (nl = +inf), whose scores may be anything, do not count.
 template <int NC, bool MASK>
 __device__ __forceinline__ void add_columns(const float* x, const float* nl, float c, int first, uint64_t (&acc)[2]) {
   const uint64_t c2 = ssa::f2_pack(c, c);
@@ -93,8 +92,8 @@ __device__ __forceinline__ void add_columns(const float* x, const float* nl, flo
       ssa::f2_unpack(e, e0, e1);
       float p0 = ex2(e0), p1 = ex2(e1);
       if (MASK) {
-        p0 = i + 2 * h >= first && (h ? l.z : l.x) > -INFINITY ? p0 : 0.f;
-        p1 = i + 2 * h + 1 >= first && (h ? l.w : l.y) > -INFINITY ? p1 : 0.f;
+        p0 = i + 2 * h >= first && (h ? l.z : l.x) != INFINITY ? p0 : 0.f;
+        p1 = i + 2 * h + 1 >= first && (h ? l.w : l.y) != INFINITY ? p1 : 0.f;
       }
       acc[h] = ssa::fadd2(acc[h], ssa::f2_pack(p0, p1));
     }
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(NT, 1)
   __shared__ uint64_t half_full[2], half_empty[2];
   __shared__ float half_sum[2][BK];
   __shared__ __align__(16) float nlse[2][N];
-  __shared__ int bare[2];  // some column has no lse
+  __shared__ int bare[2];  // some column's row has no keys
   __shared__ int pref[ssa::MAX_SEQS + 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -261,8 +260,8 @@ __global__ void __launch_bounds__(NT, 1)
       bool none = false;
 #pragma unroll 1
       for (int r = lane; r < N; r += 32) {
-        const float l = r < p.G * p.W ? neg_lse2(p, s.b, s.in, r) : -INFINITY;
-        none |= l == -INFINITY;
+        const float l = r < p.G * p.W ? neg_lse2(p, s.b, s.in, r) : INFINITY;
+        none |= l == INFINITY;
         nlse[n & 1][r] = l;
       }
       none = __any_sync(0xffffffffu, none);
@@ -463,25 +462,25 @@ __global__ void __launch_bounds__(NTP, 1)
     const uint32_t at = tmem + ((uint32_t)(32 * qd) << 16) + 64 * slice;
     const int ti = row / p.G;  // the row's token in its tile (p.tok: none)
     const float* lse = p.lse + ((size_t)b * p.Hq + hkv * p.G + row % p.G) * p.Lq;
-    // -lse in log2 units; -inf for a row that is not there or has no keys
-    auto neg_lse = [&](int g) {
+    // -inf for a row that is not there.  (Only the load, a tile ahead: arithmetic here would wait for it, 394 us
+    // against 348 for the prompt above.)
+    auto lse_of = [&](int g) {
       const int i = p.Lq - p.W + (t0 + g) * p.tok + ti;
-      const float l = g < t1 - t0 && ti < p.tok && i < p.Lq ? lse[i] : -INFINITY;
-      return l == -INFINITY ? -INFINITY : -l * LOG2E;
+      return g < t1 - t0 && ti < p.tok && i < p.Lq ? lse[i] : -INFINITY;
     };
     const uint64_t c2 = ssa::f2_pack(p.c, p.c);
     uint64_t acc[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) acc[e] = ssa::f2_pack(0.f, 0.f);
-    float next = neg_lse(0);
+    float next = lse_of(0);
 #pragma unroll 1
     for (int g = 0; g < t1 - t0; ++g) {
-      const float nl = next;
-      next = neg_lse(g + 1);
-      // keys of the slice that the row sees: the first `sees`; a row without lse none
+      const float nl = -next * LOG2E;  // +inf: a row that has no keys or is not there
+      next = lse_of(g + 1);
+      // keys of the slice that the row sees: the first `sees`; a row without keys none
       int sees = 64;
       if (p.causal) sees = min((t0 + g) * p.tok + ti + len - p.W - (j0 + 64 * slice) + 1, 64);
-      if (nl == -INFINITY) sees = 0;
+      if (nl == INFINITY) sees = 0;
       const bool mask = __any_sync(0xffffffffu, sees < 64);
       if (!__all_sync(0xffffffffu, wait(&s_full[g & 1], (g >> 1) & 1))) break;
       ssa::tc_fence_after();
@@ -496,17 +495,16 @@ __global__ void __launch_bounds__(NTP, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s_empty[g & 1]));
         }
-        if (mask) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          ssa::f2_unpack(ssa::ffma2(ssa::f2_pack(x[e], x[e + 1]), c2, nl2), x[e], x[e + 1]);
+        if (mask) {  // (the whole exponent: a score or a lse may be NaN)
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = i + e < sees ? x[e] : -INFINITY;
         }
-        // (masked: -inf, times c > 0, plus a finite number or -inf)
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float p0, p1;
-          ssa::f2_unpack(ssa::ffma2(ssa::f2_pack(x[e], x[e + 1]), c2, nl2), p0, p1);
-          acc[(i + e) / 2] = ssa::fadd2(acc[(i + e) / 2], ssa::f2_pack(ex2(p0), ex2(p1)));
-        }
+        for (int e = 0; e < 16; e += 2)
+          acc[(i + e) / 2] = ssa::fadd2(acc[(i + e) / 2], ssa::f2_pack(ex2(x[e]), ex2(x[e + 1])));
       }
     }
 #pragma unroll

@@ -361,6 +361,38 @@ def test_attn_mass_of_an_infinite_key(cache):
     assert got[0, 0, 7] == 0 and torch.isfinite(got).all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Lq,G", [(3, 4), (4, 4), (64, 4), (200, 4), (300, 7)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attn_mass_of_rows_whose_lse_is_not_a_number(cache, causal, Lq, G, value):
+    """A row with such a lse reaches the keys that it sees (NaN: makes them NaN; +inf: adds 0) and no others."""
+    d, lens = 64, _i32([333, Lq // 2])  # the second sequence's first rows lie before its first key
+    q, k = _rand(1, 2, Lq, G, d), _rand(2, 2, 340, 1, d)
+    lse = _lse(q, k, lens, causal, 0.125)
+    clean = cache.attn_mass(q.cuda(), k.cuda(), lse.cuda(), lens=lens.cuda(), causal=causal).cpu()
+    lse[0, 1, Lq // 2] = lse[1, :, 0] = lse[1, 0, Lq - 2] = -np.inf
+    _, dots, args = oracle.attn_mass(q, k, lse, lens, causal, 0.125, 0, None, 1.0)  # (the others' rounding)
+    lse[0, 1, Lq // 2] = lse[1, :, 0] = lse[1, 0, Lq - 2] = value
+    with np.errstate(invalid="ignore"):
+        want, _, _ = oracle.attn_mass(q, k, lse, lens, causal, 0.125, 0, None, 1.0)
+    got = cache.attn_mass(q.cuda(), k.cuda(), lse.cuda(), lens=lens.cuda(), causal=causal).cpu()
+    _near(got, want, d * 2.0 ** -23 * dots + 2.0 ** -22 * args + 2.0 ** -14 * want, "mass")
+    if np.isnan(value):
+        hit = torch.zeros(2, 1, 340, dtype=torch.bool)
+        hit[0, :, :333 - Lq + Lq // 2 + 1 if causal else 333] = True
+        hit[1, :, :Lq // 2 - 1 if causal else Lq // 2] = True
+        assert torch.equal(torch.isnan(got), hit)
+        assert torch.equal(got[~hit], clean[~hit])
+
+
+def test_attn_mass_of_an_infinite_score_and_lse(cache):
+    """exp(inf - inf) is NaN on that key; the others have no weight beside it."""
+    q, k = torch.full((1, 1, 1, 64), 1.0).to(BF).cuda(), _rand(2, 1, 200, 1, 64).cuda()
+    k[0, 7, 0, 3] = float("inf")
+    got = cache.attn_mass(q, k, torch.full((1, 1, 1), float("inf"), device="cuda"), causal=False)[0, 0].cpu()
+    assert torch.isnan(got[7]) and not got[:7].any() and not got[8:].any()
+
+
 # ------------------------------------------------------------------ evict
 
 EVICT = [
