@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(NT, 1)
         if (tail && !any) any_of_group(bar, false);  // the masks are in shared memory
         // x: the scores, then the exponents under the max in use.  The max only follows when a key is more
         // than 2^8 ahead (or a row has none yet): P stays below 2^8 and the sums in fp32, and the accumulators
-        // are rarely rescaled.
+        // are rarely rescaled.  Any row may send the group to FIND, but each row's max follows its own keys
+        // alone: its bits do not depend on what other rows see.
         float x[N];
         enum { CHECK, FIND, APPLY } step = force ? FIND : CHECK;
 #pragma unroll 1
@@ -468,8 +469,11 @@ __global__ void __launch_bounds__(NT, 1)
             bool empty = false;
             if (gt < N) {
               const float old = any ? row_m[wg][gt] : -INFINITY;
-              const float m = fmaxf(fmaxf(fmaxf(warp_top[wg][0][gt], warp_top[wg][1][gt]),
-                                          fmaxf(warp_top[wg][2][gt], warp_top[wg][3][gt])), old);
+              const float best = fmaxf(fmaxf(warp_top[wg][0][gt], warp_top[wg][1][gt]),
+                                       fmaxf(warp_top[wg][2][gt], warp_top[wg][3][gt]));
+              // (CHECK's own arithmetic, so that this row moves here iff it would have asked for it)
+              const bool up = old == -INFINITY || fmaf(best, c, neg_m[wg][gt]) > 8.f;
+              const float m = up ? fmaxf(best, old) : old;
               row_m[wg][gt] = m;
               empty = m == -INFINITY;
               neg_m[wg][gt] = empty ? 0.f : -m * c;
@@ -855,12 +859,14 @@ __global__ void __launch_bounds__(NT, 1)
         }
         const float tmax = fmaxf(a0, a1);
         // The max in use only follows when it is more than 2^8 behind: P stays
-        // below 2^8 and the sums in fp32, and O is rarely rescaled.
+        // below 2^8 and the sums in fp32, and O is rarely rescaled.  Each row's
+        // follows its own keys alone; operand rows that are not query rows hold
+        // what was in shared memory and do not vote.
+        const bool up = tmax * c > m * c + 8.f;
         if (t == t_first) {
           m = tmax;
-        } else if (__any_sync(0xffffffffu, tmax * c > m * c + 8.f)) {
+        } else if (__any_sync(0xffffffffu, valid && up)) {
           // (S of this tile is complete, so the P V before it is too)
-          const bool up = tmax > m;
           const float f = up ? ex2((m - tmax) * c) : 1.f;
           m = up ? tmax : m;
           l *= f;

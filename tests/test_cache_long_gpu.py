@@ -1,0 +1,125 @@
+"""GPU tests of the cache operators where a block walks several tiles of a segment
+and several segments (many more tiles than SMs), against a plain implementation
+in 64 bits on the GPU.
+
+Bounds as in test_cache_gpu.py (H = 2^-8, A the mean of |v| under the weights,
+e = d * 2^-23 * scale * max |q||k|), with the terms that grow with the length:
+at most 2^6 additions of 16 products each to an accumulator of a block, which may cut
+(2^-23 each: 2^-17), at most 2^4 rescalings (2^-22 each: 2^-18) and the merge
+of the parts (2^-20): 2^-15 A in all for the result, 2^-16 for the log-sum-exp.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_cache_gpu import BF, H, _i32, _mask, _near, _no_wait_gave_up, _rand, cache  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _tree64(q, k, v, lens, mask, scale):
+    """(out, lse, mean of |v| under the weights, largest sum of |q||k|) in 64 bits, one key head at a time."""
+    B, T, Hq, d = q.shape
+    Hkv = k.shape[2]
+    G = Hq // Hkv
+    bits = np.unpackbits(np.ascontiguousarray(mask.cpu().numpy()).view(np.uint8), axis=-1, bitorder="little")
+    bits = torch.from_numpy(bits[..., :T].astype(bool)).cuda()
+    f64 = dict(dtype=torch.float64, device="cuda")
+    out, absv = torch.zeros(B, T, Hq, d, **f64), torch.zeros(B, T, Hq, d, **f64)
+    lse, dots = torch.zeros(B, Hq, T, **f64), torch.zeros(B, Hq, T, **f64)
+    for b in range(B):
+        n = int(lens[b])
+        sees = torch.ones(T, n + T, dtype=torch.bool, device="cuda")
+        sees[:, n:] = bits[b]
+        for h in range(Hkv):
+            hq = slice(h * G, (h + 1) * G)
+            qq, kk, vv = q[b, :, hq].double(), k[b, :n + T, h].double(), v[b, :n + T, h].double()
+            x = (torch.einsum("tgd,jd->gtj", qq, kk) * scale).masked_fill(~sees, -np.inf)
+            lse[b, hq] = torch.logsumexp(x, -1)
+            w = torch.softmax(x, -1)
+            out[b, :, hq], absv[b, :, hq] = (torch.einsum("gtj,jd->tgd", w, u) for u in (vv, vv.abs()))
+            dots[b, hq] = (qq.abs() @ kk.abs().T).amax(-1).T
+    return out, lse, absv, dots
+
+
+def _check(got, q, k, v, lens, mask, scale, sums=2.0 ** -15, lse_sums=2.0 ** -16):
+    out, lse, absv, dots = (t.cpu().numpy() for t in _tree64(q, k, v, lens, mask, scale))
+    e = q.shape[3] * 2.0 ** -23 * scale * dots  # [B, Hq, T]
+    e_row = e.transpose(0, 2, 1)[..., None]
+    _near(got[0], out, H * np.abs(out) + (H + 2 * e_row + sums) * absv, "out")
+    _near(got[1], lse, e + lse_sums + 2.0 ** -18 * np.abs(lse), "lse")
+
+
+LENS = [128 * 70 + 100, 128 * 23 + 100, 128 * 60 + 100, 128 * 40 + 100]  # the draft shares its tile with 100 keys
+HKV = 8
+LONG = [  # T, query heads a key head, d: rows a key head and the kernel form they take
+    (1, 8, 128), (2, 4, 64),     # 8: few rows, 16 columns
+    (4, 8, 64), (2, 16, 128),    # 32: few rows, 32 columns
+    (7, 6, 128), (5, 8, 64),     # 42 and 40: many rows, one row tile, not full
+    (16, 4, 64), (18, 7, 128),   # 64, 126
+    (61, 4, 128), (36, 7, 64),   # 244, 252: two row tiles, not full
+    (40, 7, 64),                 # 280: two row groups
+]
+
+
+def _long(T, G, d, ramp):
+    """Scores that rise along the keys for every second row and fall for the others, by `ramp` * 2 before scaling."""
+    B, cap = len(LENS), max(LENS) + T + 3
+    tiles = HKV * sum(-(-(n + T) // 128) for n in LENS)
+    # so that blocks walk several tiles of a segment, and two segments
+    assert tiles >= 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    q, k, v = (_rand(T + i, *s, d).cuda() for i, s in enumerate(((B, T, HKV * G), (B, cap, HKV), (B, cap, HKV))))
+    sign = torch.tensor([-1.0, 1.0]).repeat(T * HKV * G + 1)[:T * HKV * G].view(T, HKV * G).cuda()
+    q[..., 0] += (20 * sign).to(BF)
+    k[..., 0] += torch.linspace(-ramp / 20, ramp / 20, cap, device="cuda")[None, :, None].to(BF)
+    return q, k, v, _i32(LENS).cuda()
+
+
+@pytest.mark.parametrize("T,G,d", LONG)
+@pytest.mark.parametrize("ramp", [0, 160])
+def test_decode_tree_of_many_tiles(cache, T, G, d, ramp):  # noqa: F811
+    """Ramp 160, scale 1/4: scores move by 80 along the keys, so rows rescale again and again, each at its own tiles."""
+    q, k, v, lens = _long(T, G, d, ramp)
+    mask = _mask("tree", len(LENS), T, T).cuda()
+    scale = 0.25 if ramp else d ** -0.5
+    got = cache.decode_tree(q, k, v, lens, mask, scale=scale)
+    _check(got, q, k, v, lens, mask, scale)
+    again = cache.decode_tree(q, k, v, lens, mask, scale=scale)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("T,G,d,before", [(7, 6, 128, 16), (5, 8, 64, 16), (18, 7, 128, 16), (36, 7, 64, 32)])
+def test_decode_tree_does_not_depend_on_what_ran_before(cache, T, G, d, before):  # noqa: F811
+    """The same bits after a call that leaves zeros in shared memory and after one that leaves large queries there."""
+    q, k, v, lens = _long(T, G, d, 0)
+    mask = _mask("chain", len(LENS), T, 0).cuda()
+    fill, fill_mask = 100 * _rand(9, len(LENS), before, HKV * 8, d).cuda(), _mask("chain", len(LENS), before, 0).cuda()
+    got = []
+    for x in (torch.zeros_like(fill), fill):
+        cache.decode_tree(x, k, v, lens, fill_mask)
+        got.append(cache.decode_tree(q, k, v, lens, mask))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("T,G,d", [t for t in LONG if t[0] > 1])
+@pytest.mark.parametrize("junk", ["aligned", float("nan"), float("inf"), 3e38])
+def test_decode_tree_hidden_keys_of_later_tiles(cache, T, G, d, junk):  # noqa: F811
+    """The last draft key, seen by the last row only, and what lies past the draft leave the others' bits alone.
+    "aligned": a score of about 45 for a row that sees the key, far ahead of every other key's."""
+    q, k, v, lens = _long(T, G, d, 20)  # rising: later tiles often bring a new, little larger, maximum
+    mask = _mask("chain", len(LENS), T, 0).cuda()
+    clean = cache.decode_tree(q, k, v, lens, mask)
+    for b, n in enumerate(LENS):
+        at = n + T - 1
+        if junk == "aligned":
+            x = q[b, T - 1].view(HKV, G, d)[:, 0].float()
+            k[b, at] = (x * 45 * d ** 0.5 / x.square().sum(-1, keepdim=True)).to(BF)
+            v[b, at] *= 100
+        else:
+            k[b, at] = v[b, at] = junk
+            k[b, at + 1:] = v[b, at + 1:] = junk
+    got = cache.decode_tree(q, k, v, lens, mask)
+    assert torch.equal(got[0][:, :T - 1], clean[0][:, :T - 1])
+    assert torch.equal(got[1][..., :T - 1], clean[1][..., :T - 1])
+    if junk == "aligned":
+        _check(got, q, k, v, lens, mask, d ** -0.5)
