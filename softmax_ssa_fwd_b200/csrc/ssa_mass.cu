@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(NT, 1)
         ssa::tc_fence_after();
         // row i of the window sits at i + len - W: key j counts from there on
         const bool mask = bare[n & 1] || (p.causal && j0 + BK - 1 > len - p.W);
-        const int first = p.causal ? (j - len + p.W) * p.G - NC * half : 0;
+        // (a distance below zero counts from row 0 on, and its product with G may not fit 32 bits)
+        const int first = p.causal ? max(j - len + p.W, 0) * p.G - NC * half : 0;
         uint64_t acc[2] = {ssa::f2_pack(0.f, 0.f), ssa::f2_pack(0.f, 0.f)};
         add_tile<NC>(lanes, &nlse[n & 1][NC * half], p.c, mask, first, acc, [&] {
           ssa::tc_fence_before();  // S is in registers: the buffer is free

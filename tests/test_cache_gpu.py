@@ -393,6 +393,16 @@ def test_attn_mass_of_an_infinite_score_and_lse(cache):
     assert torch.isnan(got[7]) and not got[:7].any() and not got[8:].any()
 
 
+@pytest.mark.parametrize("G", [8, 100])
+def test_attn_mass_of_a_cache_of_millions_of_keys(cache, G):
+    """One row of zeros with lse 0 gives every key a weight of one for each query head (100 heads, 22 million keys:
+    a key's distance times the heads does not fit 32 bits)."""
+    n = 22000000
+    q, k = torch.zeros(1, 1, G, 64, dtype=BF, device="cuda"), torch.zeros(1, n, 1, 64, dtype=BF, device="cuda")
+    got = cache.attn_mass(q, k, torch.zeros(1, G, 1, device="cuda"), lens=_i32([n - 5]).cuda())
+    assert (got[..., :-5] == G).all() and not got[..., -5:].any()
+
+
 # ------------------------------------------------------------------ evict
 
 EVICT = [
