@@ -448,12 +448,19 @@ int ssa_cache_append(const void* q, const void* k, const void* v, const int64_t*
   auto extent = [&](const int64_t* st, int heads) {
     return (size_t)((B - 1) * st[0] + (L - 1) * st[1] + (heads - 1) * st[2] + d) * 2;
   };
-  const ssa::Span in[3] = {{q, extent(strides, Hq)}, {k, extent(strides + 3, Hkv)}, {v, extent(strides + 6, Hkv)}};
+  const ssa::Span in[8] = {{q, extent(strides, Hq)},
+                           {k, extent(strides + 3, Hkv)},
+                           {v, extent(strides + 6, Hkv)},
+                           {q_weight, (size_t)d * 4},
+                           {k_weight, (size_t)d * 4},
+                           {rot > 0 ? positions : nullptr, (size_t)B * L * axes * 4},
+                           {start, (size_t)B * 4},
+                           {count, (size_t)B * 4}};
   const ssa::Span made[3] = {{k_cache, cache_bytes}, {v_cache, cache_bytes}, {q_out, out_bytes}};
   const bool in_place = q_out == q && (Hq == 1 || strides[2] == d) && (L == 1 || strides[1] == (int64_t)Hq * d) &&
                         (B == 1 || strides[0] == (int64_t)L * Hq * d);
   for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < 3; ++j)
+    for (int j = 0; j < 8; ++j)
       if (ssa::overlap(made[i], in[j]) && !(i == 2 && j == 0 && in_place)) return SSA_ERR_INVALID_ARG;
     if (ssa::overlap(made[i], made[(i + 1) % 3])) return SSA_ERR_INVALID_ARG;
   }

@@ -76,6 +76,18 @@ def test_append_outputs_over_other_tensors(cache, over):
     assert _append(cache, **over) == -1
 
 
+@pytest.mark.parametrize("out", ["out", "kc", "vc"])
+@pytest.mark.parametrize("what", ["wq", "wk", "pos", "start", "count"])
+def test_append_outputs_over_small_inputs(cache, out, what):
+    base = dict(out=0x70000, kc=0x80000, vc=0x90000)[out]
+    assert _append(cache, **{what: base}) == _append(cache, **{what: base + 0x400}) == -1
+    if not torch.cuda.is_available():  # right behind it, or not read: on to CUDA, which is not there
+        behind = base + (2 * 3 * 4 * 128 * 2 if out == "out" else 2 * 16 * 2 * 128 * 2)
+        assert _append(cache, **{what: behind}) == -3
+        if what == "pos":
+            assert _append(cache, pos=base, rot=0) == -3
+
+
 def test_append_over_its_own_queries_is_allowed(cache):
     if torch.cuda.is_available():
         pytest.skip("needs the no-GPU path")
