@@ -124,15 +124,15 @@ def _done(status, what):
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
-                     original: int = 8192, low: float = 1.0, high: float = 4.0):
+                     original: int = 8192, low: float = 1.0, high: float | None = None):
     """(inv_freq, factor) for ``append``: a CPU float64 tensor of rot / 2 radians per position, and what
     cosine and sine are multiplied by.
 
     ``scaling``: "none" base^(-2p / rot); "linear" all divided by ``factor``; "base" the base raised by
     factor^(rot / (rot - 2)), which divides the slowest by ``factor`` and leaves the fastest; "bands" by how often a
-    pair turns within ``original`` positions: at most ``low`` turns divided by ``factor``, at least ``high`` left, between
-    them a straight line between the two in turns; "ramp" the same with the line in the pair's number, and a factor of
-    1 + 0.1 ln(factor) on cosine and sine.
+    pair turns within ``original`` positions: at most ``low`` turns divided by ``factor``, at least ``high`` (None: 4) left,
+    between them a straight line between the two in turns; "ramp" the same with the line in the pair's number (``high``
+    None: 32), and a factor of 1 + 0.1 ln(factor) on cosine and sine.
     """
     _need(rot > 0 and rot % 2 == 0 and base > 0 and factor > 0, "rope_frequencies: rot even, base and factor positive")
     n = rot // 2
@@ -145,6 +145,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
         return f, 1.0
     if scaling == "linear":
         return f / factor, 1.0
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
     _need(scaling in ("bands", "ramp") and 0 < low < high and original > 0,
           "rope_frequencies: scaling is none, linear, base, bands or ramp; 0 < low < high")
     if scaling == "bands":

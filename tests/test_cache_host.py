@@ -208,6 +208,14 @@ def test_rope_frequencies(cache):
     assert (np.diff(r) <= 1e-12).all()
 
 
+def test_rope_frequencies_defaults_of_each_scaling(cache):
+    for scaling, high in (("bands", 4.0), ("ramp", 32.0)):
+        got = cache.rope_frequencies(64, scaling=scaling, factor=16.0, original=4096)
+        want = cache.rope_frequencies(64, scaling=scaling, factor=16.0, original=4096, low=1.0, high=high)
+        other = cache.rope_frequencies(64, scaling=scaling, factor=16.0, original=4096, low=1.0, high=36.0 - high)
+        assert torch.equal(got[0], want[0]) and got[1] == want[1] and not torch.equal(got[0], other[0])
+
+
 def test_rope_frequencies_refusals(cache):
     from softmax_ssa_fwd_b200 import ssa
     for kw in (dict(rot=0), dict(rot=7), dict(rot=64, base=0.0), dict(rot=64, factor=0.0), dict(rot=64, scaling="other"),
