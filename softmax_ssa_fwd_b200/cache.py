@@ -132,7 +132,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
     factor^(rot / (rot - 2)), which divides the slowest by ``factor`` and leaves the fastest; "bands" by how often a
     pair turns within ``original`` positions: at most ``low`` turns divided by ``factor``, at least ``high`` (None: 4) left,
     between them a straight line between the two in turns; "ramp" the same with the line in the pair's number (``high``
-    None: 32), and a factor of 1 + 0.1 ln(factor) on cosine and sine.
+    None: 32; the base above 1), and a factor of 1 + 0.1 ln(factor) on cosine and sine.
     """
     _need(rot > 0 and rot % 2 == 0 and base > 0 and factor > 0, "rope_frequencies: rot even, base and factor positive")
     n = rot // 2
@@ -149,6 +149,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "none", 
         high = 32.0 if scaling == "ramp" else 4.0
     _need(scaling in ("bands", "ramp") and 0 < low < high and original > 0,
           "rope_frequencies: scaling is none, linear, base, bands or ramp; 0 < low < high")
+    _need(scaling == "bands" or base > 1, "rope_frequencies: scaling 'ramp' needs a base above 1")
     if scaling == "bands":
         turns = original * f / (2 * math.pi)
         keep = ((turns - low) / (high - low)).clamp(0, 1)

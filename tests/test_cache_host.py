@@ -216,6 +216,14 @@ def test_rope_frequencies_defaults_of_each_scaling(cache):
         assert torch.equal(got[0], want[0]) and got[1] == want[1] and not torch.equal(got[0], other[0])
 
 
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_rope_frequencies_ramp_needs_falling_frequencies(cache, base):
+    from softmax_ssa_fwd_b200 import ssa
+    with pytest.raises(ssa.SSAError) as e:
+        cache.rope_frequencies(64, base, scaling="ramp", factor=2.0)
+    assert e.value.status == ssa.SSA_ERR_INVALID_ARG
+
+
 def test_rope_frequencies_refusals(cache):
     from softmax_ssa_fwd_b200 import ssa
     for kw in (dict(rot=0), dict(rot=7), dict(rot=64, base=0.0), dict(rot=64, factor=0.0), dict(rot=64, scaling="other"),
