@@ -123,3 +123,30 @@ def test_decode_tree_hidden_keys_of_later_tiles(cache, T, G, d, junk):  # noqa: 
     assert torch.equal(got[1][..., :T - 1], clean[1][..., :T - 1])
     if junk == "aligned":
         _check(got, q, k, v, lens, mask, d ** -0.5)
+
+
+# ------------------------------------------------------------------ how they are called
+
+
+def test_the_readme_generation(cache):  # noqa: F811
+    """The example as printed: the drafted tokens are in the small cache, and the rows see them."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = re.findall(r"```python\n(.*?)```", text, flags=re.S)
+    prompt, step = next(b for b in blocks if "cache.evict" in b).split("# then, per step")
+    B, L, Hq, Hkv, d, T = 2, 4200, 4, 2, 128, 6
+    zeros = lambda: torch.zeros(B, L, Hkv, d, dtype=BF, device="cuda")  # noqa: E731
+    pos = torch.arange(L + T, dtype=torch.int32, device="cuda").repeat(B, 1)
+    x = _rand(5, B, L + T, Hq + 2 * Hkv, d).cuda()
+    env = dict(zip("qkv", x[:, :L].split([Hq, Hkv, Hkv], 2)), k_cache=zeros(), v_cache=zeros(), lens=_i32([L] * B).cuda(),
+               positions=pos[:, :L].contiguous(), wq=torch.ones(d, device="cuda"), wk=torch.ones(d, device="cuda"))
+    exec(prompt, env)
+    lens = env["small"].lens.clone()
+    assert lens.tolist() == [4096] * B
+    env.update(zip("qkv", x[:, L:].split([Hq, Hkv, Hkv], 2)), positions=pos[:, L:].contiguous(),
+               tree_mask=_mask("tree", B, T, 3).cuda(), accepted=_i32([3, 1]).cuda())
+    exec("# then, per step" + step, env)
+    small = env["small"]
+    assert small.lens.tolist() == [4099, 4097] and torch.equal(small.v[:, 4096:4096 + T], x[:, L:, Hq + Hkv:])
+    _check([env["out"], env["lse"]], env["q"], small.k, small.v, lens, env["tree_mask"], d ** -0.5)
