@@ -82,7 +82,9 @@ int ssa_cache_append(const void* q, const void* k, const void* v, const int64_t*
  * log-sum-exp; a row that sees nothing gets out = 0 and lse = -inf.  Dense: no
  * key tile is skipped.  Draft rows at and past cap do not exist; bits at and past
  * T are ignored.  A key that a row does not see has no influence on it, whatever
- * it holds.
+ * it holds.  As in ssa_fwd and ssa_decode, the weights are rounded to bf16 for
+ * their product with V (a relative error of at most 2^-8 each), and their
+ * sum is of the unrounded ones; scores, maxima, sums and accumulators are fp32.
  *   q, out:    bf16 [B, T, Hq, d];  lse: fp32 [B, Hq, T]
  *   lens:      int32 [B]: cached keys before the draft
  *   tree_mask: uint32 [B, T, ceil(T / 32)]
@@ -107,7 +109,15 @@ size_t ssa_decode_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int cap, i
  * ssa_decode or ssa_decode_tree returned for these rows.  Only the last
  * `window` of the Lq rows count (0: all).  causal != 0: row i sits at position
  * i + lens[b] - Lq and gives weight to keys at and before it.  A row whose lse is
- * -inf gives none.
+ * -inf gives none; a lse of NaN makes the keys that its row sees NaN, and no others.
+ * Every key at or before a row counts, whether or not the attention looked at it:
+ * the weights are those of dense attention.  With the lse of a skip, N:M or
+ * block-mask call, or of a tree's row and branches that it does not see, they sum
+ * to more than 1.
+ * Rows padded on the right (ssa_cache_append with count[b] < L): give the length
+ * start[b] + L (at most cap), so that row i sits at start[b] + i, and a lse of -inf
+ * in the padding's rows; choose the rows that count by their lse then, not by
+ * `window`, and hold 0 in mass_in for the padding's keys.
  *   q: bf16 [B, Lq, Hq, d];  k: bf16 [B, cap, Hkv, d];  lse: fp32 [B, Hq, Lq]
  *   lens: int32 [B], NULL for cap
  *   mass_in, mass_out: fp32 [B, Hkv, cap]; mass_in NULL counts as 0 (decay is

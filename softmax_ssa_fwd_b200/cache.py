@@ -262,6 +262,9 @@ def attn_mass(q, k, lse, *, lens=None, causal=True, scale=None, window=0, mass=N
     """Attention weight that each key of k [B, cap, Hkv, d] received from the rows q [B, Lq, Hq, d] (the last
     ``window`` of them; 0: all), given their lse [B, Hq, Lq] from the attention: decay * mass + the sum over rows and
     the query heads of a key head.  Returns mass [B, Hkv, cap] fp32 (``out``; may be ``mass`` itself), 0 past lens[b].
+
+    The weights of dense attention: every key at or before a row (position i + lens[b] - Lq) counts, whether or not the
+    attention looked at it.  Rows padded on the right: lens start[b] + Lq, and a lse of -inf in the padding's rows.
     """
     B, Lq, Hq, d = _heads(q, "q")
     dev = q.get_device()

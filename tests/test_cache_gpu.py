@@ -403,6 +403,37 @@ def test_attn_mass_of_a_cache_of_millions_of_keys(cache, G):
     assert (got[..., :-5] == G).all() and not got[..., -5:].any()
 
 
+@pytest.mark.parametrize("L", [50, 200])  # 200 and 800 rows a key head: both kernels
+def test_attn_mass_of_prompts_padded_on_the_right(cache, L):
+    """As `append` leaves them with count[b] < L: every length start[b] + L, and a lse of -inf in the padding's rows."""
+    Hq, d, counts, start = 4, 64, [L, L // 3, 1], [0, 5, 20]
+    q, k = _rand(1, 3, L, Hq, d), _rand(2, 3, L + 30, 1, d)
+    lse = torch.full((3, Hq, L), -np.inf)
+    want, tol = np.zeros((3, 1, L + 30)), np.zeros((3, 1, L + 30))
+    for b, (n, s) in enumerate(zip(counts, start)):
+        one = q[b:b + 1, :n], k[b:b + 1], _i32([s + n])
+        lse[b:b + 1, :, :n] = _lse(*one, True, 0.125)
+        want[b:b + 1], dots, args = oracle.attn_mass(*one[:2], lse[b:b + 1, :, :n], one[2], True, 0.125, 0, None, 1.0)
+        tol[b:b + 1] = d * 2.0 ** -23 * dots + 2.0 ** -22 * args + 2.0 ** -14 * want[b:b + 1]
+        q[b, n:], k[b, s + n:] = float("nan"), float("nan")
+    got = cache.attn_mass(q.cuda(), k.cuda(), lse.cuda(), lens=_i32([s + L for s in start]).cuda())
+    _near(got, want, tol, "mass")
+
+
+def test_attn_mass_counts_keys_that_the_attention_left_out(cache):
+    """A chain's rows give the weights of decode_tree, a row of one sum 1; a tree's rows also count the branches that they
+    do not see, as a causal row does."""
+    B, T, Hq, Hkv, d, n = 1, 3, 2, 1, 64, 100
+    q, k, v = _rand(1, B, T, Hq, d).cuda(), _rand(2, B, n + T, Hkv, d).cuda(), _rand(3, B, n + T, Hkv, d).cuda()
+    lens = _i32([n]).cuda()
+    for mask, least in ((_mask("chain", B, T, 0), 0.0), (_i32([[[1], [2], [4]]]), 1e-3)):  # three branches of one token
+        _, lse = cache.decode_tree(q, k, v, lens, mask.cuda())
+        over = cache.attn_mass(q, k, lse, lens=lens + T).double().sum().item() - Hq * T
+        x = torch.einsum("ihd,jd->hij", q[0].double(), k[0, :, 0].double()) * d ** -0.5
+        x = torch.exp(x - lse[0].double()[..., None]).tril(n).sum().item() - Hq * T
+        assert abs(over - x) <= 1e-3 and (over >= least if least else abs(over) <= 1e-3)
+
+
 # ------------------------------------------------------------------ evict
 
 EVICT = [
