@@ -1,6 +1,7 @@
 """GPU tests of the cache operators where a block walks several tiles of a segment
 and several segments (many more tiles than SMs), against a plain implementation
-in 64 bits on the GPU.
+in 64 bits on the GPU, and of how the operators are called: captured, from
+other threads, with a workspace of the caller's.
 
 Bounds as in test_cache_gpu.py (H = 2^-8, A the mean of |v| under the weights,
 e = d * 2^-23 * scale * max |q||k|), with the terms that grow with the length:
@@ -8,6 +9,8 @@ at most 2^6 additions of 16 products each to an accumulator of a block, which ma
 (2^-23 each: 2^-17), at most 2^4 rescalings (2^-22 each: 2^-18) and the merge
 of the parts (2^-20): 2^-15 A in all for the result, 2^-16 for the log-sum-exp.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -125,7 +128,113 @@ def test_decode_tree_hidden_keys_of_later_tiles(cache, T, G, d, junk):  # noqa: 
         _check(got, q, k, v, lens, mask, d ** -0.5)
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+
+@pytest.mark.parametrize("T,Hq", [(2, 32), (16, 64)])  # 4 rows a key head: few rows; 64: many
+def test_decode_tree_past_32_bits_against_64_bits(cache, T, Hq):  # noqa: F811
+    """The second sequence of a cache of 2.9e9 elements, whose last 300 keys hold much of the weight."""
+    B, Hkv, d, cap = 2, 16, 128, 700000
+    k, v = torch.zeros(B, cap, Hkv, d, dtype=BF, device="cuda"), torch.zeros(B, cap, Hkv, d, dtype=BF, device="cuda")
+    q = _rand(1, B, T, Hq, d).cuda()
+    k[1, -300:] = 5 * _rand(2, 300, Hkv, d).cuda()
+    v[1, -300:] = _rand(3, 300, Hkv, d).cuda()
+    lens, mask = _i32([5, cap - T]).cuda(), _mask("chain", B, T, 0).cuda()
+    got = cache.decode_tree(q, k, v, lens, mask)
+    # 592 tiles a block, 296 a group: 2368 additions to an accumulator, 2^-23 each; 296 + 2^5 to a row's sum, 2^-24 each
+    _check([got[0][1:], got[1][1:]], q[1:], k[1:], v[1:], lens[1:], mask[1:], d ** -0.5, 2.0 ** -11, 2.0 ** -15)
+
+
 # ------------------------------------------------------------------ how they are called
+
+def test_append_replays_with_the_tensors_of_the_moment(cache):  # noqa: F811
+    """A captured append keeps its table of frequencies (by value) and reads positions, starts and counts anew."""
+    B, L, Hq, Hkv, d, cap = 2, 5, 8, 2, 128, 64
+    x = _rand(1, B, L, Hq + 2 * Hkv, d).cuda()
+    q, k, v = x.split([Hq, Hkv, Hkv], 2)
+    freq, factor = cache.rope_frequencies(d, 5e5, scaling="bands", factor=8.0)
+    kept = freq.clone()
+    pos, start, count = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((B, L), (B,), (B,)))
+    w = torch.randn(d, generator=torch.Generator().manual_seed(1)).cuda()
+
+    def call(f, kc, vc, out):
+        return cache.append(q, k, v, kc, vc, pos, inv_freq=f, factor=factor, q_weight=w, k_weight=w, start=start,
+                            count=count, out=out)
+
+    held, want = ([torch.zeros(B, n, h, d, dtype=BF, device="cuda") for n, h in ((cap, Hkv), (cap, Hkv), (L, Hq))]
+                  for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    call(freq, *want)
+    with torch.cuda.graph(graph):
+        call(freq, *held)
+    freq.zero_()
+    for p0, s, c in ((7, [0, 9], [5, 5]), (100000, [60, 3], [5, 2]), (0, [-2, 20], [0, 9])):
+        pos.copy_(torch.arange(L, dtype=torch.int32)[None] + p0)
+        start.copy_(_i32(s))
+        count.copy_(_i32(c))
+        x.copy_(_rand(p0 + 2, B, L, Hq + 2 * Hkv, d))
+        for t in held + want:
+            t.zero_()
+        graph.replay()
+        call(kept, *want)
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+        assert want[0].any()
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_decode_tree_in_a_workspace_of_the_caller(cache, T):  # noqa: F811
+    from softmax_ssa_fwd_b200 import ssa
+    B, Hq, Hkv, d, cap = 2, 8, 2, 128, 900
+    q, k, v = _rand(1, B, T, Hq, d).cuda(), _rand(2, B, cap, Hkv, d).cuda(), _rand(3, B, cap, Hkv, d).cuda()
+    lens, mask = _i32([100, 800]).cuda(), _mask("chain", B, T, 0).cuda()
+    want = cache.decode_tree(q, k, v, lens, mask)
+    n = cache.ssa_decode_tree_workspace_bytes(B, T, Hq, Hkv, cap, d)
+    room = torch.full((n + 256,), 0x7f, dtype=torch.uint8, device="cuda")  # junk before, a guard behind
+    for _ in range(2):
+        got = cache.decode_tree(q, k, v, lens, mask, workspace=room[:n])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (room[n:] == 0x7f).all()
+    for bad in (room[:n - 1], room[8:n + 8], room[:n].cpu(), room[:2 * (n // 2)].view(-1, 2)[:, 0]):
+        with pytest.raises(ssa.SSAError) as e:
+            cache.decode_tree(q, k, v, lens, mask, workspace=bad)
+        assert e.value.status == ssa.SSA_ERR_INVALID_ARG
+
+
+def test_calls_from_other_threads(cache):  # noqa: F811
+    """Two threads on streams of their own, at once: what one thread gets alone."""
+    B, T, Hq, Hkv, d, cap = 2, 4, 8, 2, 64, 2000
+    mask, lens = _mask("chain", B, T, 0).cuda(), _i32([1990, 700]).cuda()
+    freq, _ = cache.rope_frequencies(d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B, 1)
+
+    def steps(seed):
+        k, v = _rand(seed, B, cap, Hkv, d).cuda(), _rand(seed + 1, B, cap, Hkv, d).cuda()
+        q, kn, vn = _rand(seed + 2, B, T, Hq + 2 * Hkv, d).cuda().split([Hq, Hkv, Hkv], 2)
+        q = cache.append(q, kn, vn, k, v, pos, inv_freq=freq, start=lens)
+        out, lse = cache.decode_tree(q, k, v, lens, mask)
+        mass = cache.attn_mass(q, k, lse, lens=lens + T)
+        return [out, lse, mass, *cache.evict(k, v, mass, lens, keep=600, sink=2, recent=9)]
+
+    want = [steps(s) for s in (1, 11)]
+    torch.cuda.synchronize()
+    got, failed = [None, None], []
+
+    def work(n):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[n] = steps((1, 11)[n])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_the_readme_generation(cache):  # noqa: F811
