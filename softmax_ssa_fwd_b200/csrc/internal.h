@@ -29,7 +29,8 @@ inline bool overlap(const Span& a, const Span& b) {
 // (ssa_device_status reads and clears it); nullptr on failure.
 int* device_status_word(int dev);
 
-// The current limit of one device-side wait (ssa_set_wait_timeout_ns).
+// The current limit of one device-side wait (ssa_set_wait_timeout_ns), at most
+// 2^62, a century, so that a kernel can count it in half nanoseconds.
 unsigned long long wait_timeout_ns();
 
 }  // namespace ssa

@@ -84,7 +84,7 @@ struct SegWalk {
 struct Waiter {
   volatile int* abort;
   int* status;
-  unsigned long long limit_ns;
+  unsigned long long limit_ns;  // at most 2^62
   __device__ __forceinline__ bool operator()(const uint64_t* bar, uint32_t parity) const {
     // Counted in clocks, two a nanosecond, more than the SM makes.  An attempt sleeps for as long as the hardware
     // likes, so a wait that has outlasted the limit gives up even where its attempt succeeded.

@@ -1230,7 +1230,7 @@ int* device_status_word(int dev) {
 
 unsigned long long wait_timeout_ns() {
   std::lock_guard<std::mutex> g(g_mu);
-  return g_wait_ns;
+  return g_wait_ns < 1ull << 62 ? g_wait_ns : 1ull << 62;
 }
 
 struct Maps {

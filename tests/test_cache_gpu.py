@@ -636,3 +636,27 @@ def test_waits_that_run_out_are_reported(cache):
     o2, lse2 = cache.decode_tree(q, k, v, lens, mask)
     m2 = cache.attn_mass(q, k, lse, lens=lens), cache.attn_mass(qm, k, lm, lens=lens)
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(m[0], m2[0]) and torch.equal(m[1], m2[1])
+
+
+@pytest.mark.parametrize("ns", [2 ** 63, 2 ** 64 - 1])
+def test_a_limit_longer_than_the_clock_counts(cache, ns):
+    """Limits that stand for none do not run out at once."""
+    from softmax_ssa_fwd_b200 import ssa
+    B, T, Hq, Hkv, d, cap = 2, 8, 8, 2, 128, 2000
+    q, k, v = _rand(1, B, T, Hq, d).cuda(), _rand(2, B, cap, Hkv, d).cuda(), _rand(3, B, cap, Hkv, d).cuda()
+    lens, mask = _i32([1990, 100]).cuda(), _mask("chain", B, T, 0).cuda()
+    qm, lm = _rand(4, B, 100, Hq, d).cuda(), torch.zeros(B, Hq, 100, device="cuda")
+
+    def call():
+        o, lse = cache.decode_tree(q, k, v, lens, mask)
+        return o, lse, cache.attn_mass(q, k, lse, lens=lens), cache.attn_mass(qm, k, lm, lens=lens)
+
+    want = call()
+    ssa.ssa_set_wait_timeout_ns(ns)
+    try:
+        got = call()
+        torch.cuda.synchronize()
+    finally:
+        ssa.ssa_set_wait_timeout_ns(0)
+    assert ssa.ssa_device_status() == ssa.SSA_OK
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
