@@ -569,13 +569,20 @@ static int run(const Params& p, const void* q, const void* k, int sms, cudaStrea
 #undef SSA_STREAM
   }
   if (!ssa::tma_map_bf16_box(&mq, q, p.B, p.Lq, p.Hq, D, p.G, p.tok)) return SSA_ERR_CUDA;
-  // A cluster shares its keys' rows until there are two blocks an SM: under a
-  // causal mask a block's rows go from all to none, and few large blocks would
-  // leave SMs idle at the end.  (No further: clusters of four leave SMs of some
-  // GPCs unused.)
+  // A cluster shares its keys' rows.  Under a causal mask a block's rows go from
+  // all to none, and few large blocks would leave SMs idle at the end: two blocks
+  // share while there are fewer than two an SM, and four or eight while that
+  // still leaves fewer than two an SM, since clusters of four and eight leave SMs
+  // of some GPCs unused.  Measured at d = 128, 4 query heads a key head, clusters
+  // of 1, 2, 4, 8 (us), blocks before sharing: 16: 94 55 35 24; 48: 137 78 47 63;
+  // 64: 97 58 46 67; 128: 185 106 127 168; 256: 358 343 406 510; 768: 2,699 2,703
+  // 3,238 3,703.  Without the mask all blocks take the same time and what counts is
+  // how they divide into rounds of the SMs, which this does not work out: shared
+  // until there are two an SM (20: 218 119 68 74; 64: 98 59 66 94; 96: 141 148 126
+  // 167; 160: 436 341 306 376).
   const long long items = pairs * ((p.cap + (long long)KB - 1) / KB);
   int cs = 1;
-  while (cs < 8 && items * cs < 2 * sms && p.tiles >= cs * 4) cs *= 2;
+  while (cs < 8 && items * cs * (p.causal && cs > 1 ? 2 : 1) < 2 * sms && p.tiles >= cs * 4) cs *= 2;
   const long long grid = items * cs;
   if (grid > 0x7fffffff) return SSA_ERR_UNSUPPORTED;
   return launch(mass_prompt_kernel<D>, NTP, PromptSmem<D>::TOTAL, grid, cs, mq, mk, p, st);
