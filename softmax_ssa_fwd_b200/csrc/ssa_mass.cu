@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(NT, 1)
 
 constexpr int BN = 128;   // rows per row tile
 constexpr int KB = 256;   // keys of a block
-constexpr int NTP = 576;  // warp 0 producer, 1 MMA, 2-17 sums: 16 warps at 112 registers
+constexpr int NTP = 576;  // warp 0 producer, 1 MMA, 2-17 sums (18 warps get the registers of 20: 96, with 24 bytes spilled)
 
 template <int D>
 struct PromptSmem {
@@ -349,10 +349,11 @@ struct PromptSmem {
 // its lse is one register and its 64 sums stay in registers over all row
 // tiles, added over the threads once at the end.  (A thread a key, as in the
 // stream kernel, reads a lse from shared memory for every exponential: 352 us
-// against 340 at 8,192 rows and keys of 32 / 8 heads, d = 128.)  256 keys, because
-// every row tile comes from L2, 32 KB in the 2,048 clocks of its exponentials.
-// Those take 79 % of all clocks; a quarter of them by a polynomial on the fp32
-// pipe changed nothing, so what is left lies between tiles and blocks.
+// against 340 at 8,192 rows and keys of 32 / 8 heads, d = 128; 344 since a lse of
+// NaN is kept to the keys that its row sees.)  256 keys, because every row tile
+// comes from L2, 32 KB in the 2,048 clocks of its exponentials.  Those take 78 % of
+// all clocks; a quarter of them by a polynomial on the fp32 pipe changed nothing,
+// so what is left lies between tiles and blocks.
 template <int D>
 __global__ void __launch_bounds__(NTP, 1)
     mass_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(NTP, 1)
     const int ti = row / p.G;  // the row's token in its tile (p.tok: none)
     const float* lse = p.lse + ((size_t)b * p.Hq + hkv * p.G + row % p.G) * p.Lq;
     // -inf for a row that is not there.  (Only the load, a tile ahead: arithmetic here would wait for it, 394 us
-    // against 348 for the prompt above.)
+    // against 348 in a row of calls at the sizes above.)
     auto lse_of = [&](int g) {
       const int i = p.Lq - p.W + (t0 + g) * p.tok + ti;
       return g < t1 - t0 && ti < p.tok && i < p.Lq ? lse[i] : -INFINITY;
